@@ -22,7 +22,7 @@ STATUS = {
     4: "out of memory", 5: "device wait timed out", 6: "plan does not match the call",
     7: "no sm_100 device", 8: "index outside its table (debug build check)",
 }
-BF16, F32 = 0, 1
+BF16, F32, F16 = 0, 1, 2
 QK_BF16, QK_E4M3 = 0, 1          # storage of the permuted Q and K (Plan.set_qk_format)
 
 # exported names of include/ultragen.h
@@ -38,6 +38,10 @@ SYMBOLS = (
     "ultragen_plan_set_qk_format", "ultragen_plan_set_lr_order",
     "ultragen_plan_set_clock_record", "ultragen_plan_read_clock",
     "ultragen_plan_export_halo_ops", "ultragen_plan_export_items",
+    "ultragen_layer_norm", "ultragen_layer_norm_backward_workspace", "ultragen_layer_norm_backward",
+    "ultragen_adapter_project_workspace", "ultragen_adapter_project",
+    "ultragen_cross_attention_workspace", "ultragen_cross_attention",
+    "ultragen_cross_attention_backward",
 )
 
 
@@ -64,6 +68,27 @@ class PlanInfo(ctypes.Structure):
         d = {f: getattr(self, f) for f, _ in self._fields_}
         d["rope_axes"] = tuple(self.rope_axes)
         return d
+
+
+class NormSizes(ctypes.Structure):
+    """ultragen_norm_t."""
+    _fields_ = [(f, ctypes.c_int32) for f in ("batch", "rows", "cols", "dtype", "wdtype",
+                                              "per_sample", "plus_one")] + \
+        [("eps", ctypes.c_float)] + \
+        [(f, ctypes.c_int64) for f in ("x_row", "x_batch", "y_row", "y_batch", "dy_row", "dy_batch")]
+
+
+class AdapterSizes(ctypes.Structure):
+    """ultragen_adapter_t."""
+    _fields_ = [(f, ctypes.c_int32) for f in ("rows", "k", "n", "rank", "adapters", "dtype")] + \
+        [("x_row", ctypes.c_int64), ("y_row", ctypes.c_int64)]
+
+
+class CrossSizes(ctypes.Structure):
+    """ultragen_cross_t."""
+    _fields_ = [(f, ctypes.c_int32) for f in ("batch", "nq", "ns", "heads", "kv_heads", "head_dim",
+                                              "dtype")] + \
+        [("scale", ctypes.c_float), ("stride", (ctypes.c_int64 * 3) * 8)]
 
 
 class UltragenError(RuntimeError):
@@ -117,6 +142,16 @@ def lib() -> ctypes.CDLL:
     L.ultragen_host_runner_forward.argtypes = [vp, vp, vp, vp, vp, vp]
     L.ultragen_host_runner_last_launch_count.argtypes = [vp]
     L.ultragen_host_runner_destroy.argtypes = [vp]
+    size, psize = ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)
+    norm, adapter, cross = (ctypes.POINTER(t) for t in (NormSizes, AdapterSizes, CrossSizes))
+    L.ultragen_layer_norm.argtypes = [norm] + [vp] * 7
+    L.ultragen_layer_norm_backward_workspace.argtypes = [norm, psize]
+    L.ultragen_layer_norm_backward.argtypes = [norm] + [vp] * 8 + [cint, vp, size, vp]
+    L.ultragen_adapter_project_workspace.argtypes = [adapter, psize]
+    L.ultragen_adapter_project.argtypes = [adapter] + [vp] * 9 + [size, vp]
+    L.ultragen_cross_attention_workspace.argtypes = [cross, cint, psize]
+    L.ultragen_cross_attention.argtypes = [cross] + [vp] * 8 + [size, vp]
+    L.ultragen_cross_attention_backward.argtypes = [cross] + [vp] * 12 + [size, vp]
     for name in SYMBOLS:
         if name != "ultragen_status_string":
             getattr(L, name).restype = cint

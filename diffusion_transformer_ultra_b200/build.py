@@ -22,7 +22,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libultragen.so")
 DEBUG_LIB = os.path.join(HERE, "libultragen_debug.so")
 
-SOURCES = ["plan.cpp", "api.cu", "permute.cu", "hla_fwd.cu", "noalloc.cu", "warm_start.cu", "host_runner.cu"]
+SOURCES = ["plan.cpp", "api.cu", "permute.cu", "hla_fwd.cu", "noalloc.cu", "warm_start.cu", "host_runner.cu",
+           "layer_norm.cu", "adapter.cu", "cross_attention.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -247,6 +247,8 @@ int sm_count() {
   return n > 0 ? n : 148;
 }
 
+int current_device(int* dev) { return check_device(dev); }
+
 int ensure_device_tables(ultragen_plan_t* p) { return ensure_device(p); }
 
 size_t split_workspace_bytes(const ultragen_plan_t* p, int64_t units) {

@@ -63,7 +63,9 @@ enum ultragen_status {
                                      tile coordinate outside its table or tensor             */
 };
 
-enum ultragen_dtype { ULTRAGEN_BF16 = 0, ULTRAGEN_F32 = 1 };
+/* F16 is taken by the operators around the attention (layer norm, adapter projection, cross
+ * attention); the permute and unpermute passes take BF16 and F32. */
+enum ultragen_dtype { ULTRAGEN_BF16 = 0, ULTRAGEN_F32 = 1, ULTRAGEN_F16 = 2 };
 
 /* Storage of the permuted Q and K (ultragen_plan_set_qk_format). */
 enum ultragen_qk_format { ULTRAGEN_QK_BF16 = 0, ULTRAGEN_QK_E4M3 = 1 };
@@ -414,6 +416,116 @@ int ultragen_host_runner_destroy(ultragen_host_runner_t* runner);
 int ultragen_warm_start(const float* x_lr, const float* noise, float* x_hr, int batch,
                         int channels, int h, int w, int H, int W, float alpha, float sharpen,
                         uint64_t seed, uint64_t offset, ultragen_stream_t stream);
+
+/*
+ * Operators around the attention.  The pages place the joint attention behind projections that
+ * carry a low-rank adapter for the LR tokens ([UG-note] 关键设计 3) inside an MMDiT block; the
+ * calls below are what stands directly in front of it and beside it.  They take strided
+ * tensors: every stride is in elements, the last dimension is contiguous, and no operand may
+ * overlap itself.  They hold no state between calls: a call that needs scratch memory takes a
+ * workspace (16-byte aligned device memory of at least the bytes its _workspace function
+ * returns for the same sizes on the same device), which it may overwrite and which must not be
+ * shared by calls that overlap on the GPU.  Sizes of zero are allowed where noted.
+ */
+
+/*
+ * ultragen_layer_norm -- y = (x - mean) * rstd * w' + bias over the last dimension, with
+ * mean = sum(x) / cols, rstd = (sum((x - mean)^2) / cols + eps)^-1/2, and w' = weight, or
+ * 1 + weight (plus_one), or 1 (weight NULL).
+ *   x, y          [batch, rows, cols] of dtype; element (b, i, c) at b * batch stride + i * row
+ *                 stride + c.  y may be x.
+ *   weight, bias  [cols], or [batch, cols] with per_sample, contiguous, of wdtype (dtype or
+ *                 F32); each may be NULL
+ *   mean, rstd    [batch * rows] F32 outputs, each may be NULL
+ * All arithmetic is fp32; y is rounded once.  batch = 0 and rows = 0 do nothing.
+ *   INVALID_ARG: null x / y, a negative size, cols < 1, an unknown type, eps negative or not
+ *   finite.  UNSUPPORTED: cols > 16384, batch * rows > 2^31 - 1, batch > 65535 with per_sample.
+ *
+ * ultragen_layer_norm_backward -- for g = dy * w' and xh = (x - mean) * rstd:
+ *   dx = rstd (g - sum(g) / cols - xh sum(g xh) / cols), dweight = sum of dy xh and dbias = sum
+ *   of dy over all rows (over each sample's rows with per_sample).
+ *   dy, x, dx     as x above, each with its own strides (dx: y_row / y_batch); dx may be dy or x
+ *   mean, rstd    as the forward pass wrote them
+ *   dweight, dbias  shaped as weight, of grad_dtype (any); each may be NULL; the sums are fp32
+ *                 in a fixed order (the same inputs give the same bits)
+ *   workspace     needed only when dweight or dbias is given
+ */
+typedef struct {
+  int32_t batch, rows, cols;
+  int32_t dtype, wdtype;      /* of x, y, dy, dx; of weight and bias */
+  int32_t per_sample;         /* weight and bias are [batch, cols] */
+  int32_t plus_one;           /* w' = 1 + weight */
+  float eps;
+  int64_t x_row, x_batch, y_row, y_batch, dy_row, dy_batch;
+} ultragen_norm_t;
+int ultragen_layer_norm(const ultragen_norm_t* n, const void* x, const void* weight, const void* bias,
+                        void* y, float* mean, float* rstd, ultragen_stream_t stream);
+int ultragen_layer_norm_backward_workspace(const ultragen_norm_t* n, size_t* bytes);
+int ultragen_layer_norm_backward(const ultragen_norm_t* n, const void* dy, const void* x,
+                                 const void* weight, const float* mean, const float* rstd, void* dx,
+                                 void* dweight, void* dbias, int grad_dtype, void* workspace,
+                                 size_t workspace_bytes, ultragen_stream_t stream);
+
+/*
+ * ultragen_adapter_project -- a projection shared by all rows with each row's own low-rank
+ * adapter beside it ([UG-note] 关键设计 3: LoRA on the LR tokens' Q/K/V, the HR projection
+ * unchanged):  y_m = W x_m + bias + scales[id] B_id (A_id x_m),  id = ids[m].
+ *   x [rows, k], y [rows, n]   of dtype (BF16, F16 or F32), row strides x_row, y_row
+ *   w [n, k], bias [n] (may be NULL), a [adapters, rank, k], b [adapters, n, rank]  of dtype,
+ *                 contiguous
+ *   scales [adapters] F32 (NULL: 1)
+ *   ids [rows] int32: the row's adapter; any value outside [0, adapters) means none.  Rows of
+ *                 one adapter need not be neighbours.
+ * Sums are fp32; y is rounded once.  rows = 0 does nothing.
+ *   INVALID_ARG: a null pointer, a size < 1 (rows < 0), an unknown type, too little workspace.
+ *   UNSUPPORTED: rank > 128, n > 4,194,240.
+ */
+typedef struct {
+  int32_t rows, k, n, rank, adapters, dtype;
+  int64_t x_row, y_row;
+} ultragen_adapter_t;
+int ultragen_adapter_project_workspace(const ultragen_adapter_t* c, size_t* bytes);
+int ultragen_adapter_project(const ultragen_adapter_t* c, const void* x, const void* w, const void* bias,
+                             const void* a, const void* b, const float* scales, const int32_t* ids,
+                             void* y, void* workspace, size_t workspace_bytes, ultragen_stream_t stream);
+
+/*
+ * ultragen_cross_attention -- attention of nq queries over another sequence of ns keys and
+ * values (an encoder's states): o_i = sum_j p_ij v_j, p_i = softmax over the visible keys of
+ * scale q_i . k_j.
+ *   q, o          [batch, nq, heads, head_dim], k, v [batch, ns, kv_heads, head_dim] of dtype
+ *                 (BF16 or F16); query head h reads key/value head h / (heads / kv_heads)
+ *   stride[t]     batch, row and head stride of tensor t, in the order q, k, v, o, do, dq, dk,
+ *                 dv; pointers and strides are multiples of 16 bytes
+ *   kv_lens       [batch] int32 or NULL: keys [0, kv_lens[b]) of sample b are visible (clamped
+ *                 to [0, ns]); key_mask [batch, ns] bytes or NULL: nonzero = visible.  What
+ *                 hidden keys and values hold does not matter (NaN included).
+ *   lse           [batch, heads, nq] F32 or NULL: log(sum_j exp(scale q_i . k_j)), natural
+ *   A query without a visible key gets o = 0 and lse = -inf.
+ * ultragen_cross_attention_backward -- the gradients of a loss with d_o = dLoss/do; o and lse as
+ *   the forward pass wrote them.  Hidden keys and values get zeros; a query without a visible
+ *   key gets dq = 0.  dk and dv of a shared head are summed over its query heads.  Results do
+ *   not depend on timing (no atomics on the outputs).
+ * Products run on 16-bit tensor cores with fp32 sums; softmax statistics are fp32.  batch, nq or
+ * ns = 0 is allowed (outputs that exist are written).  workspace: `backward` selects the call.
+ *   INVALID_ARG: null pointers, negative sizes, heads not a multiple of kv_heads, misaligned
+ *   strides, too little workspace.  UNSUPPORTED: another dtype or head_dim (64, 128), more than
+ *   128 query heads per key/value head, sizes past int32 limits.
+ */
+typedef struct {
+  int32_t batch, nq, ns, heads, kv_heads, head_dim, dtype;
+  float scale;
+  int64_t stride[8][3];
+} ultragen_cross_t;
+int ultragen_cross_attention_workspace(const ultragen_cross_t* c, int backward, size_t* bytes);
+int ultragen_cross_attention(const ultragen_cross_t* c, const void* q, const void* k, const void* v,
+                             const int32_t* kv_lens, const uint8_t* key_mask, void* o, float* lse,
+                             void* workspace, size_t workspace_bytes, ultragen_stream_t stream);
+int ultragen_cross_attention_backward(const ultragen_cross_t* c, const void* d_o, const void* q,
+                                      const void* k, const void* v, const void* o, const float* lse,
+                                      const int32_t* kv_lens, const uint8_t* key_mask, void* dq, void* dk,
+                                      void* dv, void* workspace, size_t workspace_bytes,
+                                      ultragen_stream_t stream);
 
 #ifdef __cplusplus
 }
