@@ -41,7 +41,7 @@ SYMBOLS = (
     "ultragen_layer_norm", "ultragen_layer_norm_backward_workspace", "ultragen_layer_norm_backward",
     "ultragen_adapter_project_workspace", "ultragen_adapter_project",
     "ultragen_cross_attention_workspace", "ultragen_cross_attention",
-    "ultragen_cross_attention_backward",
+    "ultragen_cross_attention_backward", "ultragen_operator_status",
 )
 
 
@@ -87,7 +87,7 @@ class AdapterSizes(ctypes.Structure):
 class CrossSizes(ctypes.Structure):
     """ultragen_cross_t."""
     _fields_ = [(f, ctypes.c_int32) for f in ("batch", "nq", "ns", "heads", "kv_heads", "head_dim",
-                                              "dtype")] + \
+                                              "dtype", "masked")] + \
         [("scale", ctypes.c_float), ("stride", (ctypes.c_int64 * 3) * 8)]
 
 
@@ -151,6 +151,7 @@ def lib() -> ctypes.CDLL:
     L.ultragen_adapter_project.argtypes = [adapter] + [vp] * 9 + [size, vp]
     L.ultragen_cross_attention_workspace.argtypes = [cross, cint, psize]
     L.ultragen_cross_attention.argtypes = [cross] + [vp] * 8 + [size, vp]
+    L.ultragen_operator_status.argtypes = [vp]
     L.ultragen_cross_attention_backward.argtypes = [cross] + [vp] * 12 + [size, vp]
     for name in SYMBOLS:
         if name != "ultragen_status_string":

@@ -83,6 +83,13 @@ def _stream(device):
     return torch.cuda.current_stream(device).cuda_stream
 
 
+def operator_status(stream=None) -> int:
+    """Waits for `stream` (default: the current one), then returns and clears the device-side
+    status of this module's operators on the current device (0: no kernel's wait ran out)."""
+    s = torch.cuda.current_stream() if stream is None else stream
+    return lib().ultragen_operator_status(s.cuda_stream)
+
+
 # ------------------------------------------------------------------------------- layer norm
 def _batched(t):
     return t if t.dim() == 3 else t.unsqueeze(0)
@@ -232,6 +239,7 @@ def _cross_sizes(q, k, v, kv_lens, key_mask, scale):
     if key_mask is not None:
         _contiguous(key_mask, "key_mask", (torch.bool, torch.uint8), (B, S), q.device)
     return CrossSizes(batch=B, nq=Nq, ns=S, heads=H, kv_heads=G, head_dim=D, dtype=_CODE[q.dtype],
+                      masked=0 if key_mask is None else 1,
                       scale=float(D ** -0.5 if scale is None else scale))
 
 

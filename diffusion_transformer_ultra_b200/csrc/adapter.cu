@@ -7,6 +7,7 @@
 #include <algorithm>
 #include <cstdint>
 
+#include "device.h"
 #include "elem.cuh"
 #include "kernels.h"
 #include "nvtx_range.h"

@@ -7,6 +7,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "device.h"
 #include "kernels.h"
 #include "nvtx_range.h"
 #include "warm_fused.h"
@@ -168,11 +169,6 @@ int cuda_status(cudaError_t e) {
 }
 
 }  // namespace
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 EncodeTiledFn encode_fn() {
   static EncodeTiledFn fn = nullptr;

@@ -142,8 +142,6 @@ int make_tmap(CUtensorMap* m, const void* base, uint64_t rows, int D);
 int make_tmap_u8(CUtensorMap* m, const void* base, uint64_t rows, int D);
 // Streaming multiprocessors of the current device (api.cu).
 int sm_count();
-// The current device, or ULTRAGEN_ERR_NO_DEVICE when it is not an sm_100 one (api.cu).
-int current_device(int* dev);
 cudaError_t launch_warm_start(const WarmArgs& a, cudaStream_t st);
 // Launches the block-sparse attention kernel; tensor maps are built by the caller.
 // qk8 = 1: tmQ and tmK are byte maps of e4m3 Q and K (D = 128 only).

@@ -23,6 +23,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "device.h"
 #include "elem.cuh"
 #include "kernels.h"
 #include "nvtx_range.h"

@@ -514,7 +514,8 @@ int ultragen_adapter_project(const ultragen_adapter_t* c, const void* x, const v
  */
 typedef struct {
   int32_t batch, nq, ns, heads, kv_heads, head_dim, dtype;
-  float scale;
+  int32_t masked;             /* 1: the calls pass a key_mask (sizes the workspace) */
+  float scale;                /* finite, > 0 */
   int64_t stride[8][3];
 } ultragen_cross_t;
 int ultragen_cross_attention_workspace(const ultragen_cross_t* c, int backward, size_t* bytes);
@@ -526,6 +527,10 @@ int ultragen_cross_attention_backward(const ultragen_cross_t* c, const void* d_o
                                       const int32_t* kv_lens, const uint8_t* key_mask, void* dq, void* dk,
                                       void* dv, void* workspace, size_t workspace_bytes,
                                       ultragen_stream_t stream);
+
+/* Waits for `stream`, then reports (and clears) a device-side error of the operators around the
+ * attention on the current device: ULTRAGEN_ERR_TIMEOUT if a kernel's wait ran out (limit 2 s). */
+int ultragen_operator_status(ultragen_stream_t stream);
 
 #ifdef __cplusplus
 }
