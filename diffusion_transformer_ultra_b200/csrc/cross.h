@@ -32,8 +32,8 @@ struct CrossParams {
   const void* o;                   // dQ kernel: o and do of the rows, for delta
   const void* d_o;
   int64_t o_st[3], do_st[3];
-  float* lse;                      // [batch][heads][nq] or null
-  float* delta;                    // backward: [batch][heads][nq]
+  float* lse;                      // [batch][heads][nq]; forward: output or null, backward: input
+  float* delta;                    // backward: [batch][heads][nq], written by the dQ kernel
   float* part;                     // partial results of split items (null: nsplit == 1)
   int part_rows;                   // rows stored per (unit, query tile, split)
   unsigned long long timeout_ns;
@@ -52,5 +52,7 @@ cudaError_t launch_cross_dkv(const CrossMaps& m, const CrossParams& p, int dtype
 // Device error words of the kernels: read and cleared, in stream order; waits for `s`.
 cudaError_t cross_fwd_status(int* code, cudaStream_t s);
 cudaError_t cross_bwd_status(int* code, cudaStream_t s);
+// Reads `symbol` (a device int) after the work of `s`, and clears it if it is set.
+cudaError_t read_clear_error(const void* symbol, int* code, cudaStream_t s);
 
 }  // namespace ug

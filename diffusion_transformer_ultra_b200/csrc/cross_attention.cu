@@ -3,8 +3,8 @@
 //   p_ij = exp(s_ij - lse_i),  o_i = sum_j p_ij v_j
 //   delta_i = do_i . o_i,  ds_ij = p_ij (do_i . v_j - delta_i)
 //   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i p_ij do_i
-// This file holds the entry points, the schedule of the forward pass, and the small kernels beside
-// the tensor-core ones (cross_fwd.cu): the bit words of a key mask and the join of split rows.
+// This file holds the entry points, the schedules, and the small kernels beside the tensor-core ones
+// (cross_fwd.cu, cross_bwd.cu): the bit words of a key mask and the join of split query rows.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -22,42 +22,6 @@
 
 namespace ug {
 namespace {
-
-struct CrossArgs {
-  const void* p[8];             // q, k, v, o, do, dq, dk, dv
-  int64_t st[8][3];             // batch, row and head strides
-  float* lse;
-  const int32_t* lens;
-  const uint8_t* mask;
-  int batch, nq, ns, heads, kv_heads, group;
-  float scale;
-};
-
-template <typename T>
-__device__ __forceinline__ T* at(const CrossArgs& a, int which, int b, int64_t row, int h) {
-  return const_cast<T*>(static_cast<const T*>(a.p[which])) + b * a.st[which][0] + row * a.st[which][1] +
-         h * a.st[which][2];
-}
-
-__device__ __forceinline__ int visible_len(const CrossArgs& a, int b) {
-  return a.lens ? max(0, min(a.ns, a.lens[b])) : a.ns;
-}
-__device__ __forceinline__ bool hidden(const CrossArgs& a, int b, int j) {
-  return a.mask && !a.mask[(int64_t)b * a.ns + j];
-}
-
-template <typename T, int D>
-__device__ __forceinline__ void load_row(const T* p, float (&v)[D / 32]) {
-#pragma unroll
-  for (int c = 0; c < D / 32; ++c) v[c] = to_f32(p[(threadIdx.x & 31) + 32 * c]);
-}
-template <int D>
-__device__ __forceinline__ float dot(const float (&a)[D / 32], const float (&b)[D / 32]) {
-  float s = 0.f;
-#pragma unroll
-  for (int c = 0; c < D / 32; ++c) s += a[c] * b[c];
-  return warp_sum(s);
-}
 
 // Bit words of the visible keys of each sample (mask and length), and whether exactly one is.
 // One block per sample.
@@ -113,62 +77,6 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const CrossParams p) {
   if (p.lse && lane == 0) p.lse[r] = sum == 0.f ? neg_inf() : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(256) cross_dq_kernel(const CrossArgs a) {
-  const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (r >= (int64_t)a.batch * a.heads * a.nq) return;
-  const int i = r % a.nq, h = r / a.nq % a.heads, b = r / a.nq / a.heads;
-  float q[D / 32], g[D / 32], dq[D / 32] = {}, t[D / 32], v[D / 32];
-  load_row<T, D>(at<T>(a, 0, b, i, h), q);
-  load_row<T, D>(at<T>(a, 4, b, i, h), g);
-  load_row<T, D>(at<T>(a, 3, b, i, h), t);
-  const float delta = dot<D>(g, t), lse = a.lse[r];
-  const int len = lse == -INFINITY ? 0 : visible_len(a, b);
-  for (int j = 0; j < len; ++j) {
-    if (hidden(a, b, j)) continue;
-    load_row<T, D>(at<T>(a, 1, b, j, h / a.group), t);
-    load_row<T, D>(at<T>(a, 2, b, j, h / a.group), v);
-    const float ds = expf(a.scale * dot<D>(q, t) - lse) * (dot<D>(g, v) - delta) * a.scale;
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c) dq[c] += ds * t[c];
-  }
-  T* out = at<T>(a, 5, b, i, h);
-#pragma unroll
-  for (int c = 0; c < D / 32; ++c) out[(threadIdx.x & 31) + 32 * c] = from_f32<T>(dq[c]);
-}
-
-template <typename T, int D>
-__global__ void __launch_bounds__(256) cross_dkv_kernel(const CrossArgs a) {
-  const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (r >= (int64_t)a.batch * a.kv_heads * a.ns) return;
-  const int j = r % a.ns, hk = r / a.ns % a.kv_heads, b = r / a.ns / a.kv_heads;
-  float k[D / 32] = {}, v[D / 32] = {}, dk[D / 32] = {}, dv[D / 32] = {}, q[D / 32], g[D / 32], t[D / 32];
-  if (j < visible_len(a, b) && !hidden(a, b, j)) {
-    load_row<T, D>(at<T>(a, 1, b, j, hk), k);
-    load_row<T, D>(at<T>(a, 2, b, j, hk), v);
-    for (int h = hk * a.group; h < (hk + 1) * a.group; ++h)
-      for (int i = 0; i < a.nq; ++i) {
-        load_row<T, D>(at<T>(a, 0, b, i, h), q);
-        load_row<T, D>(at<T>(a, 4, b, i, h), g);
-        load_row<T, D>(at<T>(a, 3, b, i, h), t);
-        const float p = expf(a.scale * dot<D>(q, k) - a.lse[((int64_t)b * a.heads + h) * a.nq + i]);
-        const float ds = p * (dot<D>(g, v) - dot<D>(g, t)) * a.scale;
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          dk[c] += ds * q[c];
-          dv[c] += p * g[c];
-        }
-      }
-  }
-  T* ok = at<T>(a, 6, b, j, hk);
-  T* ov = at<T>(a, 7, b, j, hk);
-#pragma unroll
-  for (int c = 0; c < D / 32; ++c) {
-    ok[(threadIdx.x & 31) + 32 * c] = from_f32<T>(dk[c]);
-    ov[(threadIdx.x & 31) + 32 * c] = from_f32<T>(dv[c]);
-  }
-}
-
 int check(const ultragen_cross_t* c) {
   if (!c || c->batch < 0 || c->nq < 0 || c->ns < 0 || c->heads < 1 || c->kv_heads < 1) return ULTRAGEN_ERR_INVALID_ARG;
   if (c->heads % c->kv_heads != 0 || !std::isfinite(c->scale) || !(c->scale > 0.f)) return ULTRAGEN_ERR_INVALID_ARG;
@@ -179,29 +87,13 @@ int check(const ultragen_cross_t* c) {
   return ULTRAGEN_OK;
 }
 
-CrossArgs args_of(const ultragen_cross_t* c, const int32_t* lens, const uint8_t* mask) {
-  CrossArgs a = {};
-  for (int t = 0; t < 8; ++t)
-    for (int d = 0; d < 3; ++d) a.st[t][d] = c->stride[t][d];
-  a.lens = lens;
-  a.mask = mask;
-  a.batch = c->batch;
-  a.nq = c->nq;
-  a.ns = c->ns;
-  a.heads = c->heads;
-  a.kv_heads = c->kv_heads;
-  a.group = c->heads / c->kv_heads;
-  a.scale = c->scale;
-  return a;
-}
-
 int status_of(cudaError_t e) { return e == cudaSuccess ? ULTRAGEN_OK : ULTRAGEN_ERR_CUDA; }
 
 // Bytes of the workspace's parts, each a multiple of 16: bit words and single flags of a key mask,
-// then the partial results of split items.
+// then (backward) delta, then the partial results of split items.
 struct Layout {
-  size_t words, single, part;
-  size_t total() const { return words + single + part; }
+  size_t words, single, delta, part;
+  size_t total() const { return words + single + delta + part; }
 };
 size_t pad16(size_t n) { return (n + 15) & ~size_t(15); }
 
@@ -231,14 +123,47 @@ void schedule(const ultragen_cross_t* c, int sms, CrossParams& p) {
   p.part_rows = p.nqt == 1 ? p.group * c->nq : 128;
 }
 
-Layout forward_layout(const ultragen_cross_t* c, CrossParams& p) {
-  schedule(c, sm_count(), p);
+Layout mask_layout(const ultragen_cross_t* c) {
   Layout l = {};
   if (c->masked) {
     l.words = (size_t)c->batch * ((c->ns + 127) / 128) * 16;
     l.single = pad16((size_t)c->batch * 4);
   }
+  return l;
+}
+
+Layout forward_layout(const ultragen_cross_t* c, CrossParams& p) {
+  schedule(c, sm_count(), p);
+  Layout l = mask_layout(c);
   if (p.nsplit > 1) l.part = pad16((size_t)p.units * p.nqt * p.nsplit * p.part_rows * (c->head_dim + 1) * 4);
+  return l;
+}
+
+// Schedule of the dK/dV kernel: an item is a key tile and a range of the query tiles.  The ranges
+// are split when the key tiles alone would not fill the multiprocessors evenly: the cost is taken
+// as the rounds of items, each of its query tiles and about two tiles' time to begin and end; a
+// split adds the fp32 partials' way through memory, about one tile's time per item on top, and
+// about three for the join kernel.
+Layout backward_layout(const ultragen_cross_t* c, CrossParams& p) {
+  const int sms = sm_count();
+  p.units = c->batch * c->kv_heads;
+  p.group = c->heads / c->kv_heads;
+  p.toks = 128 / p.group;
+  p.nqt = (c->nq + p.toks - 1) / p.toks;
+  const int64_t tiles = (int64_t)p.units * ((c->ns + 127) / 128);
+  int64_t best = 0;
+  p.nsplit = p.nqt > 0 ? 1 : 0;
+  for (int n = 1; n <= std::min(p.nqt, 64); ++n) {
+    const int64_t cost = (tiles * n + sms - 1) / sms * ((p.nqt + n - 1) / n + (n > 1 ? 3 : 2)) + (n > 1 ? 3 : 0);
+    if (n == 1 || cost < best) {
+      best = cost;
+      p.nsplit = n;
+    }
+  }
+  p.total = (int)(tiles * p.nsplit);
+  Layout l = mask_layout(c);
+  l.delta = pad16((size_t)c->batch * c->heads * c->nq * 4);
+  if (p.nsplit > 1) l.part = (size_t)p.total * 2 * 128 * c->head_dim * 4;
   return l;
 }
 
@@ -292,15 +217,19 @@ cudaError_t pack_mask(const ultragen_cross_t* c, const int32_t* lens, const uint
   return cudaGetLastError();
 }
 
-template <typename T, int D>
-cudaError_t backward(const CrossArgs& a, cudaStream_t s) {
-  const int64_t n = (int64_t)a.batch * a.heads * a.nq, m = (int64_t)a.batch * a.kv_heads * a.ns;
-  if (n) cross_dq_kernel<T, D><<<(unsigned)((n + 7) / 8), 256, 0, s>>>(a);
-  if (m) cross_dkv_kernel<T, D><<<(unsigned)((m + 7) / 8), 256, 0, s>>>(a);
-  return cudaGetLastError();
+}  // namespace
+
+cudaError_t read_clear_error(const void* symbol, int* code, cudaStream_t s) {
+  const int zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbolAsync(code, symbol, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e == cudaSuccess && *code) {
+    e = cudaMemcpyToSymbolAsync(symbol, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  }
+  return e;
 }
 
-}  // namespace
 }  // namespace ug
 
 using namespace ug;
@@ -312,7 +241,9 @@ int ultragen_cross_attention_workspace(const ultragen_cross_t* c, int backward, 
   if (st != ULTRAGEN_OK) return st;
   if (!bytes || (backward != 0 && backward != 1)) return ULTRAGEN_ERR_INVALID_ARG;
   CrossParams p = {};
-  *bytes = backward || c->batch == 0 || c->nq == 0 ? 0 : forward_layout(c, p).total();
+  if (c->batch == 0) *bytes = 0;
+  else if (backward) *bytes = backward_layout(c, p).total();
+  else *bytes = c->nq == 0 ? 0 : forward_layout(c, p).total();
   return ULTRAGEN_OK;
 }
 
@@ -362,8 +293,10 @@ int ultragen_cross_attention(const ultragen_cross_t* c, const void* q, const voi
 int ultragen_operator_status(ultragen_stream_t stream) {
   int dev, st, code = 0;
   if ((st = current_device(&dev)) != ULTRAGEN_OK) return st;
+  int back = 0;
   if ((st = status_of(cross_fwd_status(&code, reinterpret_cast<cudaStream_t>(stream))))) return st;
-  return code ? ULTRAGEN_ERR_TIMEOUT : ULTRAGEN_OK;
+  if ((st = status_of(cross_bwd_status(&back, reinterpret_cast<cudaStream_t>(stream))))) return st;
+  return code || back ? ULTRAGEN_ERR_TIMEOUT : ULTRAGEN_OK;
 }
 
 int ultragen_cross_attention_backward(const ultragen_cross_t* c, const void* d_o, const void* q, const void* k,
@@ -376,18 +309,53 @@ int ultragen_cross_attention_backward(const ultragen_cross_t* c, const void* d_o
   if (c->batch == 0) return ULTRAGEN_OK;
   if (c->nq > 0 && (!d_o || !q || !o || !lse || !dq)) return ULTRAGEN_ERR_INVALID_ARG;
   if (c->ns > 0 && (!k || !v || !dk || !dv)) return ULTRAGEN_ERR_INVALID_ARG;
+  const int64_t(*sd)[3] = c->stride;
+  if (c->nq > 0 && (!aligned(q, sd[0]) || !aligned(o, sd[3]) || !aligned(d_o, sd[4]) || !aligned(dq, sd[5])))
+    return ULTRAGEN_ERR_INVALID_ARG;
+  if (c->ns > 0 && (!aligned(k, sd[1]) || !aligned(v, sd[2]) || !aligned(dk, sd[6]) || !aligned(dv, sd[7])))
+    return ULTRAGEN_ERR_INVALID_ARG;
+  if (key_mask && !c->masked) return ULTRAGEN_ERR_INVALID_ARG;
+  if (c->ns == 0) key_mask = nullptr;
+  CrossParams p = {};
+  const Layout l = backward_layout(c, p);
+  if (l.total() > 0 && (!workspace || workspace_bytes < l.total() || ((uintptr_t)workspace & 15u))) return ULTRAGEN_ERR_INVALID_ARG;
   int dev;
   if ((st = current_device(&dev)) != ULTRAGEN_OK) return st;
-  (void)workspace;
-  (void)workspace_bytes;
-  CrossArgs a = args_of(c, kv_lens, key_mask);
-  const void* ptrs[8] = {q, k, v, o, d_o, dq, dk, dv};
-  std::copy(ptrs, ptrs + 8, a.p);
-  a.lse = const_cast<float*>(lse);
+  common(c, kv_lens, key_mask, l, workspace, p);
+  p.o = o;
+  p.d_o = d_o;
+  std::copy(sd[3], sd[3] + 3, p.o_st);
+  std::copy(sd[4], sd[4] + 3, p.do_st);
+  p.lse = const_cast<float*>(lse);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.delta = reinterpret_cast<float*>(ws + l.words + l.single);
+  alignas(64) CrossMaps m;
+  std::memset(&m, 0, sizeof(m));
+  if (c->nq > 0 &&
+      ((st = make_map(&m.q, q, sd[0], c->dtype, c->batch, c->nq, c->kv_heads, p.group, c->head_dim, p.toks)) ||
+       (st = make_map(&m.d_o, d_o, sd[4], c->dtype, c->batch, c->nq, c->kv_heads, p.group, c->head_dim, p.toks))))
+    return st;
+  if (c->ns > 0 &&
+      ((st = make_map(&m.k, k, sd[1], c->dtype, c->batch, c->ns, c->kv_heads, 1, c->head_dim, 128)) ||
+       (st = make_map(&m.v, v, sd[2], c->dtype, c->batch, c->ns, c->kv_heads, 1, c->head_dim, 128))))
+    return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (c->dtype == ULTRAGEN_BF16)
-    return status_of(c->head_dim == 128 ? backward<__nv_bfloat16, 128>(a, s) : backward<__nv_bfloat16, 64>(a, s));
-  return status_of(c->head_dim == 128 ? backward<__half, 128>(a, s) : backward<__half, 64>(a, s));
+  if (key_mask && (st = status_of(pack_mask(c, kv_lens, key_mask, p, s)))) return st;
+  if (c->nq > 0) {
+    CrossParams pq = p;
+    pq.nsplit = 1;
+    pq.total = p.units * p.nqt;
+    pq.out[0] = dq;
+    std::copy(sd[5], sd[5] + 3, pq.out_st[0]);
+    if ((st = status_of(launch_cross_dq(m, pq, c->dtype, c->head_dim, std::min(pq.total, sm_count()), s)))) return st;
+  }
+  if (c->ns == 0) return ULTRAGEN_OK;
+  p.out[0] = dk;
+  p.out[1] = dv;
+  std::copy(sd[6], sd[6] + 3, p.out_st[0]);
+  std::copy(sd[7], sd[7] + 3, p.out_st[1]);
+  p.part = l.part ? reinterpret_cast<float*>(ws + l.words + l.single + l.delta) : nullptr;
+  return status_of(launch_cross_dkv(m, p, c->dtype, c->head_dim, std::min(p.total, sm_count()), s));
 }
 
 }  // extern "C"

@@ -1,0 +1,939 @@
+// Cross attention backward for sm_100a (tcgen05 + TMEM + TMA), two kernels:
+//   dQ:     per 128-row query tile, over its key tiles:  S = Q K^T, dP = dO V^T,
+//           dS = P (dP - delta), dQ += dS K.  Also makes delta for the second kernel.
+//   dK/dV:  per 128-key tile, over query tiles:  S^T = K Q^T, dP^T = V dO^T,
+//           dV += P^T dO, dK += dS^T Q.
+// P = exp2(scale log2(e) S - lse log2(e)) from the forward pass's lse, so no running maximum.
+// The split in two costs S and dP twice (seven products per pair of tiles instead of five) and
+// saves the sum of dQ over key tiles through memory: with the 512 keys of a prompt that would be
+// four fp32 copies of dQ, eight times the bytes of all the operands.
+// P and dS pass through TMEM as 16-bit A operands (the tensor core's type); sums, P's exponent
+// and dS before its rounding are fp32.
+//
+// Roles of both kernels: warps 0-7 the elementwise part (two warpgroups; warp w has the rows of
+// TMEM lane quarter w % 4 and half the columns), warp 8 producer (TMA), warp 9 MMA issuer.
+// Steps of consecutive items run on without a drain: the products of a step are issued around
+// the one before it, so that the tensor core works while the elementwise part of a step runs.
+#include <cstdint>
+#include <mutex>
+
+#include "cross.cuh"
+
+namespace ug {
+namespace {
+
+__device__ int g_error;                // first wait that ran out since the last status read
+
+constexpr int kWarpProducer = 8, kWarpMma = 9, kWarpAux = 10;
+constexpr uint64_t kDrainNs = 50ull * 1000 * 1000;   // bounded drain on the abort path
+constexpr int BOX_BYTES = 128 * 64 * 2;
+
+// Slot and wait parity of the n-th use of a ring of N slots.
+template <int N>
+struct Ring {
+  uint32_t n = 0;
+  __device__ __forceinline__ uint32_t slot() const { return n % N; }
+  __device__ __forceinline__ uint32_t phase() const { return (n / N) & 1; }
+};
+
+struct Waiter {
+  uint32_t bar;                        // first barrier
+  volatile int* abort_flag;
+  int code;
+  uint64_t timeout_ns;
+  __device__ __forceinline__ bool operator()(int b, uint32_t parity) const {
+    return mbar_wait(bar + 8 * b, parity, abort_flag, &g_error, code, timeout_ns);
+  }
+  // all lanes of the warp
+  __device__ __forceinline__ bool warp(int b, uint32_t parity) const {
+    return __all_sync(0xffffffffu, (*this)(b, parity));
+  }
+  __device__ __forceinline__ void drain(int b, uint32_t parity) const {
+    mbar_wait(bar + 8 * b, parity, nullptr, &g_error, DEV_TIMEOUT_DRAIN, kDrainNs);
+  }
+};
+
+// Waits (bounded) for the copies in flight of a ring of N slots at barrier b: none may land after
+// this CTA exits.
+template <int N>
+__device__ __forceinline__ void drain_ring(const Waiter& wait, int b, const Ring<N>& r) {
+  for (uint32_t i = r.n >= N ? r.n - N : 0; i < r.n; ++i) wait.drain(b + i % N, (i / N) & 1);
+}
+
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+// One [128 x D] tile: D / 64 boxes of 64 elements.  `head_row`: the row coordinate.
+template <int D>
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* m, int row, int hk, int b, uint32_t bar) {
+#pragma unroll
+  for (int bx = 0; bx < D / 64; ++bx) tma_load_5d(dst + bx * BOX_BYTES, m, bx * 64, 0, row, hk, b, bar);
+}
+
+// D[128 x 128] = A B^T over K = D, both tiles K-major.
+template <typename T, int D>
+__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b) {
+  const uint32_t alo = desc_lo(a, 16), blo = desc_lo(b, 16);
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) {
+    const uint32_t off = ((kk / 4) * BOX_BYTES + (kk % 4) * 32) >> 4;
+    mma_ss_w(d, alo + off, blo + off, desc_hi_sw128(1024), idesc_half<T>(128, 128, 0), kk > 0 ? 1u : 0u);
+  }
+}
+
+// D[128 x D] (+)= A B: A is a packed 16-bit operand in TMEM, its columns 64 h .. 64 h + 63 at
+// column a + 64 h (32 columns); B a [128 x D] tile read MN-major.
+template <typename T, int D>
+__device__ __forceinline__ void mma_accum(uint32_t d, uint32_t a, uint32_t b, bool first) {
+  const uint32_t blo = desc_lo(b, BOX_BYTES);
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk)
+    mma_ts_w(d, a + (kk / 4) * 64 + (kk % 4) * 8, blo + kk * (2048 >> 4), desc_hi_sw128(1024), idesc_half<T>(128, D, 1),
+             (first && kk == 0) ? 0u : 1u);
+}
+
+// Half a row of an accumulator, scaled and rounded, to 16-bit global memory.
+template <typename T, int D>
+__device__ __forceinline__ void store_half(uint32_t tmem, T* dst, float f, bool on) {
+#pragma unroll
+  for (int ch = 0; ch < D / 64; ++ch) {
+    uint32_t o[32];
+    __syncwarp();
+    tmem_ld32_sync(tmem + ch * 32, o);
+    if (!on) continue;
+    uint4* out = reinterpret_cast<uint4*>(dst + ch * 32);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint4 v;
+      v.x = pack2<T>(__uint_as_float(o[8 * q + 0]) * f, __uint_as_float(o[8 * q + 1]) * f);
+      v.y = pack2<T>(__uint_as_float(o[8 * q + 2]) * f, __uint_as_float(o[8 * q + 3]) * f);
+      v.z = pack2<T>(__uint_as_float(o[8 * q + 4]) * f, __uint_as_float(o[8 * q + 5]) * f);
+      v.w = pack2<T>(__uint_as_float(o[8 * q + 6]) * f, __uint_as_float(o[8 * q + 7]) * f);
+      out[q] = v;
+    }
+  }
+}
+
+template <typename T, int D>
+__device__ __forceinline__ void zero_half(T* dst) {
+#pragma unroll
+  for (int q = 0; q < D / 16; ++q) reinterpret_cast<uint4*>(dst)[q] = make_uint4(0, 0, 0, 0);
+}
+
+// -lse log2(e), the constant of a row's exponentials; -inf (P = 0) for a row that does not exist
+// or has no visible key.
+__device__ __forceinline__ float neg_lse2(float lse) { return lse == neg_inf() ? neg_inf() : -lse * 1.4426950408889634f; }
+
+// ---------------------------------------------------------------------------------- dQ
+// 512 threads: warps 10 (scrubber: zeroes hidden K rows, which may hold NaN: 0 * NaN), 12-15
+// (delta = do . o of the next items' rows, from global memory, two items ahead).
+// TMEM: S [0,128), dP / dS in two buffers [128,384), dQ [384,384+D).
+template <int D>
+struct CfgQ {
+  static constexpr int TILE = 128 * D * 2;
+  static constexpr int NK = D == 128 ? 3 : 5, NV = D == 128 ? 2 : 4;
+  static constexpr int DO_OFF = TILE, K_OFF = 2 * TILE, V_OFF = K_OFF + NK * TILE;
+  static constexpr int RED_OFF = V_OFF + NV * TILE;            // [2][2][128] floats: halves of a row's sum
+  static constexpr int BAR_OFF = RED_OFF + 4 * 128 * 4;
+  // full / empty of Q, dO, K (full, scrubbed, empty), V; S ready / read; dP ready; dS ready;
+  // accumulator ready / read; delta ready / read; halves exchanged
+  static constexpr int B_QF = 0, B_QE = 1, B_OF = 2, B_OE = 3, B_KF = 4, B_KS = B_KF + NK, B_KE = B_KS + NK, B_VF = B_KE + NK,
+                       B_VE = B_VF + NV, B_SF = B_VE + NV, B_SR = B_SF + 1, B_PF = B_SR + 1, B_DS = B_PF + 2, B_AF = B_DS + 1,
+                       B_AE = B_AF + 1, B_DF = B_AE + 1, B_DE = B_DF + 2, B_XR = B_DE + 2, B_DRAIN = B_XR + 1,
+                       NBAR = B_DRAIN + 1;
+  static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
+  static constexpr int SMEM = MISC_OFF + 16;
+  static_assert(SMEM <= 227 * 1024, "shared memory per CTA exceeds 227 KB");
+  static __device__ __forceinline__ uint32_t arrivals(int i) {
+    if (i == B_SR || i == B_DS || i == B_AE || i == B_XR || i == B_DE || i == B_DE + 1) return 8;   // elementwise warps
+    return i == B_DF || i == B_DF + 1 ? 4 : 1;                                                       // delta warps
+  }
+};
+constexpr int kThreadsQ = 512, kRegsLaunchQ = 128, kRegsElemQ = 184, kRegsOtherQ = 72;
+static_assert(256 * kRegsElemQ + 256 * kRegsOtherQ <= kThreadsQ * kRegsLaunchQ, "register split exceeds the launch allocation");
+
+struct ItemQ {
+  int b, hk, qt, len, n;
+  __device__ __forceinline__ ItemQ(const CrossParams& p, int it) {
+    qt = it % p.nqt;
+    const int u = it / p.nqt;
+    b = u / p.kv_heads;
+    hk = u - b * p.kv_heads;
+    len = cross_len(p, b);
+    n = (len + 127) >> 7;
+  }
+};
+
+template <int D>
+__device__ void dq_producer(const CrossMaps& m, const CrossParams& p, uint32_t sbase, const Waiter& wait) {
+  using C = CfgQ<D>;
+  const uint32_t bar = wait.bar;
+  const int q_bytes = p.toks * p.group * D * 2;
+  Ring<1> rq, ro;
+  Ring<C::NK> rk;
+  Ring<C::NV> rv;
+  bool ok = true;
+  for (int it = blockIdx.x; ok && it < p.total; it += gridDim.x) {
+    const ItemQ w(p, it);
+    for (int j = 0; j < w.n; ++j) {
+      if (j == 0) {
+        if (!(ok = wait(C::B_QE, rq.phase() ^ 1))) break;
+        mbar_expect_tx(bar + 8 * C::B_QF, q_bytes);
+        load_tile<D>(sbase, &m.q, w.qt * p.toks, w.hk, w.b, bar + 8 * C::B_QF);
+        ++rq.n;
+      }
+      const uint32_t ks = rk.slot(), vs = rv.slot();
+      if (!(ok = wait(C::B_KE + ks, rk.phase() ^ 1))) break;
+      mbar_expect_tx(bar + 8 * (C::B_KF + ks), C::TILE);
+      load_tile<D>(sbase + C::K_OFF + ks * C::TILE, &m.k, j * 128, w.hk, w.b, bar + 8 * (C::B_KF + ks));
+      ++rk.n;
+      if (j == 0) {
+        if (!(ok = wait(C::B_OE, ro.phase() ^ 1))) break;
+        mbar_expect_tx(bar + 8 * C::B_OF, q_bytes);
+        load_tile<D>(sbase + C::DO_OFF, &m.d_o, w.qt * p.toks, w.hk, w.b, bar + 8 * C::B_OF);
+        ++ro.n;
+      }
+      if (!(ok = wait(C::B_VE + vs, rv.phase() ^ 1))) break;
+      mbar_expect_tx(bar + 8 * (C::B_VF + vs), C::TILE);
+      load_tile<D>(sbase + C::V_OFF + vs * C::TILE, &m.v, j * 128, w.hk, w.b, bar + 8 * (C::B_VF + vs));
+      ++rv.n;
+    }
+  }
+  if (!ok) {
+    drain_ring(wait, C::B_QF, rq);
+    drain_ring(wait, C::B_OF, ro);
+    drain_ring(wait, C::B_KF, rk);
+    drain_ring(wait, C::B_VF, rv);
+  }
+}
+
+template <int D>
+__device__ void dq_scrub(const CrossParams& p, uint32_t sbase, const Waiter& wait) {
+  using C = CfgQ<D>;
+  Ring<C::NK> rk;
+  for (int it = blockIdx.x; it < p.total; it += gridDim.x) {
+    const ItemQ w(p, it);
+    for (int j = 0; j < w.n; ++j, ++rk.n) {
+      const uint4 vis = cross_words(p, w.b, j, w.len);
+      if (!wait.warp(C::B_KF + rk.slot(), rk.phase())) return;
+      if (!all_visible(vis)) {
+        scrub_rows<D>(sbase + C::K_OFF + rk.slot() * C::TILE, BOX_BYTES, vis, 0, 128);
+        fence_async_smem();
+      }
+      warp_arrive(wait.bar + 8 * (C::B_KS + rk.slot()));
+    }
+  }
+}
+
+// delta of the rows of items with more than one key tile (see dq_elementwise), to global memory.
+// Four warps, 32 rows each; D / 8 lanes per row.
+template <typename T, int D>
+__device__ void dq_delta(const CrossParams& p, const Waiter& wait) {
+  using C = CfgQ<D>;
+  constexpr int LPR = D / 8, RPW = 32 / LPR;            // lanes per row, rows per load
+  const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  Ring<2> rd;
+  for (int it = blockIdx.x; it < p.total; it += gridDim.x) {
+    const ItemQ w(p, it);
+    if (w.n < 2) continue;
+    if (!wait.warp(C::B_DE + rd.slot(), rd.phase() ^ 1)) return;
+#pragma unroll 1
+    for (int r0 = 0; r0 < 32; r0 += 4 * RPW) {
+      uint4 a[4] = {}, g[4] = {};
+      int64_t row[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = warp * 32 + r0 + i * RPW + lane / LPR;
+        const int tr = r / p.group, tok = w.qt * p.toks + tr, h = w.hk * p.group + r - tr * p.group;
+        row[i] = -1;
+        if (tr < p.toks && tok < p.nq) {
+          row[i] = ((int64_t)w.b * p.heads + h) * p.nq + tok;
+          const int c = lane % LPR * 8;
+          a[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.o) + w.b * p.o_st[0] + tok * p.o_st[1] + h * p.o_st[2] + c));
+          g[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.d_o) + w.b * p.do_st[0] + tok * p.do_st[1] +
+                                                      h * p.do_st[2] + c));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const T* av = reinterpret_cast<const T*>(&a[i]);
+        const T* gv = reinterpret_cast<const T*>(&g[i]);
+        float s = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s += to_f32(av[e]) * to_f32(gv[e]);
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane % LPR == 0 && row[i] >= 0) p.delta[row[i]] = s;
+      }
+    }
+    warp_arrive(wait.bar + 8 * (C::B_DF + rd.slot()));
+    ++rd.n;
+  }
+}
+
+template <typename T, int D>
+__device__ void dq_mma(const CrossParams& p, uint32_t sbase, uint32_t tbase, const Waiter& wait) {
+  using C = CfgQ<D>;
+  const uint32_t bar = wait.bar, tAcc = tbase + 384;
+  const int kready = p.scrub ? C::B_KS : C::B_KF;
+  Ring<1> rq;
+  Ring<C::NK> rk;
+  Ring<C::NV> rv;
+  uint32_t g = 0, items = 0;           // steps and items begun
+  bool ok = true, pending = false, pfirst = false, plast = false;
+  uint32_t pslot = 0, pitem = 0;
+  // dQ += dS K of step g - 1
+  auto accumulate = [&]() {
+    if (!wait(C::B_DS, (g - 1) & 1)) return false;
+    if (pfirst && pitem > 0 && !wait(C::B_AE, (pitem - 1) & 1)) return false;
+    tc_fence_after();
+    mma_accum<T, D>(tAcc, tbase + 128 + 128 * ((g - 1) & 1), sbase + C::K_OFF + pslot * C::TILE, pfirst);
+    mma_commit(bar + 8 * (C::B_KE + pslot));
+    if (plast) mma_commit(bar + 8 * C::B_AF);
+    return true;
+  };
+  for (int it = blockIdx.x; ok && it < p.total; it += gridDim.x) {
+    const ItemQ w(p, it);
+    for (int j = 0; j < w.n; ++j) {
+      if (j == 0 && !(ok = wait(C::B_QF, rq.phase()))) break;
+      if (!(ok = wait(kready + rk.slot(), rk.phase()))) break;
+      if (g > 0 && !(ok = wait(C::B_SR, (g - 1) & 1))) break;
+      tc_fence_after();
+      mma_scores<T, D>(tbase, sbase, sbase + C::K_OFF + rk.slot() * C::TILE);
+      mma_commit(bar + 8 * C::B_SF);
+      if (j == w.n - 1) mma_commit(bar + 8 * C::B_QE);
+      if (j == 0 && !(ok = wait(C::B_OF, rq.phase()))) break;
+      if (!(ok = wait(C::B_VF + rv.slot(), rv.phase()))) break;
+      tc_fence_after();
+      // (overwrites dS of step g - 2, which the product issued before has read)
+      mma_scores<T, D>(tbase + 128 + 128 * (g & 1), sbase + C::DO_OFF, sbase + C::V_OFF + rv.slot() * C::TILE);
+      mma_commit(bar + 8 * (C::B_PF + (g & 1)));
+      mma_commit(bar + 8 * (C::B_VE + rv.slot()));
+      if (j == w.n - 1) mma_commit(bar + 8 * C::B_OE);
+      if (pending && !(ok = accumulate())) break;
+      pending = true;
+      pfirst = j == 0;
+      plast = j == w.n - 1;
+      pslot = rk.slot();
+      pitem = items;
+      ++rk.n;
+      ++rv.n;
+      ++g;
+    }
+    if (w.n > 0) {
+      ++rq.n;
+      ++items;
+    }
+  }
+  if (ok && pending) ok = accumulate();
+  if (!ok) {
+    mma_commit(bar + 8 * C::B_DRAIN);
+    wait.drain(C::B_DRAIN, 0);
+  }
+}
+
+template <typename T, int D>
+__device__ void dq_elementwise(const CrossParams& p, float* red, uint32_t tbase, const Waiter& wait) {
+  using C = CfgQ<D>;
+  const uint32_t bar = wait.bar;
+  const int half = threadIdx.x >> 7, r = threadIdx.x & 127;
+  const uint32_t lane_off = (uint32_t)((threadIdx.x >> 5) & 3) * 32u << 16;
+  const uint32_t tS = tbase + lane_off + half * 64, tP = tS + 128, tAcc = tbase + lane_off + 384 + half * (D / 2);
+  const int tok_r = r / p.group, g_r = r - tok_r * p.group;
+  const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
+  uint32_t g = 0, items = 0, xn = 0;
+  Ring<2> rd;
+  T* pend = nullptr;                   // dq row of the item whose accumulator is still to be read
+  bool pending = false, pend_on = false;
+  auto finish = [&]() {
+    if (!wait.warp(C::B_AF, (items - 1) & 1)) return false;
+    tc_fence_after();
+    store_half<T, D>(tAcc, pend, p.scale, pend_on);
+    tc_fence_before();
+    warp_arrive(bar + 8 * C::B_AE);
+    pending = false;
+    return true;
+  };
+  for (int it = blockIdx.x; it < p.total; it += gridDim.x) {
+    const ItemQ w(p, it);
+    const int tok = w.qt * p.toks + tok_r, h = w.hk * p.group + g_r;
+    const bool real = tok_r < p.toks && tok < p.nq;
+    T* out = static_cast<T*>(p.out[0]) + w.b * p.out_st[0][0] + tok * p.out_st[0][1] + h * p.out_st[0][2] + half * (D / 2);
+    if (w.n == 0) {
+      if (real) zero_half<T, D>(out);
+      continue;
+    }
+    const int64_t row = ((int64_t)w.b * p.heads + h) * p.nq + tok;
+    const float nl = real ? neg_lse2(__ldg(p.lse + row)) : neg_inf();
+    const float2 nl2 = make_float2(nl, nl);
+    // one visible key has weight one whatever its logit: dS is zero exactly
+    const bool zero = w.len == 1 || (p.single && __ldg(p.single + w.b));
+    float nd = 0.f;                    // -delta
+    if (w.n > 1) {
+      if (!wait.warp(C::B_DF + rd.slot(), rd.phase())) return;
+      if (real) nd = -__ldcg(p.delta + row);
+      warp_arrive(bar + 8 * (C::B_DE + rd.slot()));
+      ++rd.n;
+    }
+    for (int j = 0; j < w.n; ++j) {
+      const uint4 vis = cross_words(p, w.b, j, w.len);
+      const uint32_t w0 = half ? vis.z : vis.x, w1 = half ? vis.w : vis.y;
+      const bool part = (w0 & w1) != ~0u;
+      uint32_t s[64];
+      if (!wait.warp(C::B_SF, g & 1)) return;
+      tc_fence_after();
+      tmem_ld64_sync(tS, s);
+      tc_fence_before();
+      warp_arrive(bar + 8 * C::B_SR);
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        const float2 x = ffma2(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), scale2, nl2);
+        s[2 * c] = __float_as_uint(ex2(x.x));
+        s[2 * c + 1] = __float_as_uint(ex2(x.y));
+      }
+      if (!wait.warp(C::B_PF + (g & 1), (g >> 1) & 1)) return;
+      tc_fence_after();
+      uint32_t d[64];
+      tmem_ld64_sync(tP + 128 * (g & 1), d);
+      if (part) {                      // whatever hidden keys and values hold
+#pragma unroll
+        for (int c = 0; c < 64; ++c)
+          if (!(((c < 32 ? w0 : w1) >> (c & 31)) & 1u)) s[c] = d[c] = 0u;
+      }
+      if (w.n == 1) {
+        // all of a row's keys are here: delta = sum_j p_j dP_j, without the rounding of o, which
+        // matters where few keys share the weight
+        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          sum = ffma2(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])),
+                      make_float2(__uint_as_float(d[2 * c]), __uint_as_float(d[2 * c + 1])), sum);
+        // two buffers: the next exchange's writers may be ahead of this one's readers
+        float* x = red + (xn & 1) * 256;
+        x[half * 128 + r] = sum.x + sum.y;
+        warp_arrive(bar + 8 * C::B_XR);
+        if (!wait.warp(C::B_XR, xn & 1)) return;
+        const float delta = x[r] + x[128 + r];
+        ++xn;
+        nd = -delta;
+        if (real && half == 0) p.delta[row] = delta;
+      }
+      const float2 nd2 = make_float2(nd, nd);
+      uint32_t pk[32];
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        const float2 x = fmul2(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])),
+                               fadd2(make_float2(__uint_as_float(d[2 * c]), __uint_as_float(d[2 * c + 1])), nd2));
+        pk[c] = zero ? 0u : pack2<T>(x.x, x.y);
+      }
+      __syncwarp();
+      tmem_st32(tP + 128 * (g & 1), pk);
+      tmem_wait_st();
+      tc_fence_before();
+      warp_arrive(bar + 8 * C::B_DS);
+      ++g;
+      // the item before: its last product runs while this item's first step is worked on
+      if (pending && !finish()) return;
+    }
+    ++items;
+    pending = true;
+    pend = out;
+    pend_on = real;
+  }
+  if (pending) finish();
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreadsQ, 1) cross_dq_kernel(const __grid_constant__ CrossMaps m, const CrossParams p) {
+  using C = CfgQ<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  if (sbase & 1023) {                  // the swizzle needs it; the declaration asks for it
+    if (threadIdx.x == 0) atomicExch(&g_error, (int)DEV_TIMEOUT_PRODUCER);
+    return;
+  }
+  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
+  const uint32_t bar = sbase + C::BAR_OFF;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::NBAR; ++i) mbar_init(bar + 8 * i, C::arrivals(i));
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (p.toks * p.group < 128) {        // rows that no copy fills are read by the products
+    uint4* q = reinterpret_cast<uint4*>(smem);
+    for (int i = threadIdx.x; i < 2 * C::TILE / 16; i += kThreadsQ) q[i] = make_uint4(0, 0, 0, 0);
+    fence_async_smem();
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(smem_u32(misc), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = misc[0];
+  Waiter wait{bar, abort_flag, DEV_TIMEOUT_SOFTMAX, p.timeout_ns};
+  if (warp >= 8) {
+    regs_shrink<kRegsOtherQ>();
+    if (warp == kWarpProducer) {
+      wait.code = DEV_TIMEOUT_PRODUCER;
+      if (lane == 0) dq_producer<D>(m, p, sbase, wait);
+    } else if (warp == kWarpMma) {
+      wait.code = DEV_TIMEOUT_MMA;
+      if (lane == 0) dq_mma<T, D>(p, sbase, tbase, wait);
+    } else if (warp == kWarpAux) {
+      if (p.scrub) dq_scrub<D>(p, sbase, wait);
+    } else if (warp >= 12) {
+      dq_delta<T, D>(p, wait);
+    }
+  } else {
+    regs_grow<kRegsElemQ>();
+    dq_elementwise<T, D>(p, reinterpret_cast<float*>(smem + C::RED_OFF), tbase, wait);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kWarpMma) {
+    __syncwarp();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------------- dK, dV
+// 384 threads: warp 10 brings each step's -lse log2(e) and -delta into shared memory.
+// TMEM: S^T / P^T [0,128), dP^T / dS^T [128,256), dV [256,256+D), dK [256+D,256+2D).
+template <int D>
+struct CfgK {
+  static constexpr int TILE = 128 * D * 2;
+  static constexpr int NQ = D == 128 ? 3 : 4, NO = D == 128 ? 2 : 4, NA = D == 128 ? 2 : 4;
+  static constexpr int V_OFF = TILE, Q_OFF = 2 * TILE, DO_OFF = Q_OFF + NQ * TILE;
+  static constexpr int AUX_OFF = DO_OFF + NO * TILE;           // [NA][2][128] floats
+  static constexpr int BAR_OFF = AUX_OFF + NA * 2 * 128 * 4;
+  // full / empty of K, V, Q, dO and the row constants; S ready; P stored; dP ready; dS stored;
+  // accumulators ready / read
+  static constexpr int B_KF = 0, B_KE = 1, B_VF = 2, B_VE = 3, B_QF = 4, B_QE = B_QF + NQ, B_OF = B_QE + NQ, B_OE = B_OF + NO,
+                       B_XF = B_OE + NO, B_XE = B_XF + NA, B_SF = B_XE + NA, B_PS = B_SF + 1, B_PF = B_PS + 1, B_DS = B_PF + 1,
+                       B_AF = B_DS + 1, B_AE = B_AF + 1, B_DRAIN = B_AE + 1, NBAR = B_DRAIN + 1;
+  static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
+  static constexpr int SMEM = MISC_OFF + 16;
+  static_assert(SMEM <= 227 * 1024, "shared memory per CTA exceeds 227 KB");
+  static __device__ __forceinline__ uint32_t arrivals(int i) {
+    return i == B_PS || i == B_DS || i == B_AE || (i >= B_XE && i < B_XE + NA) ? 8 : 1;   // 8 elementwise warps
+  }
+};
+constexpr int kThreadsK = 384, kRegsLaunchK = 168, kRegsElemK = 208, kRegsOtherK = 80;
+static_assert(256 * kRegsElemK + 128 * kRegsOtherK <= kThreadsK * kRegsLaunchK, "register split exceeds the launch allocation");
+
+// Work item: key tiles fastest (neighbours in time share the query tiles in L2), then the split of
+// the query tiles, then units.  Query tiles [q0, q1); none when every key is behind `len`.
+struct ItemK {
+  int b, hk, kt, split, len, q0, q1;
+  __device__ __forceinline__ ItemK(const CrossParams& p, int it) {
+    const int nkt = (p.ns + 127) >> 7;
+    kt = it % nkt;
+    it /= nkt;
+    split = it % p.nsplit;
+    const int u = it / p.nsplit;
+    b = u / p.kv_heads;
+    hk = u - b * p.kv_heads;
+    len = cross_len(p, b);
+    q0 = (int)((int64_t)p.nqt * split / p.nsplit);
+    q1 = kt * 128 < len ? (int)((int64_t)p.nqt * (split + 1) / p.nsplit) : q0;
+  }
+};
+
+template <int D>
+__device__ void dkv_producer(const CrossMaps& m, const CrossParams& p, uint32_t sbase, const Waiter& wait) {
+  using C = CfgK<D>;
+  const uint32_t bar = wait.bar;
+  const int q_bytes = p.toks * p.group * D * 2;
+  Ring<1> rk, rv;
+  Ring<C::NQ> rq;
+  Ring<C::NO> ro;
+  bool ok = true;
+  for (int it = blockIdx.x; ok && it < p.total; it += gridDim.x) {
+    const ItemK w(p, it);
+    for (int i = w.q0; i < w.q1; ++i) {
+      if (i == w.q0) {
+        if (!(ok = wait(C::B_KE, rk.phase() ^ 1))) break;
+        mbar_expect_tx(bar + 8 * C::B_KF, C::TILE);
+        load_tile<D>(sbase, &m.k, w.kt * 128, w.hk, w.b, bar + 8 * C::B_KF);
+        ++rk.n;
+      }
+      const uint32_t qs = rq.slot(), os = ro.slot();
+      if (!(ok = wait(C::B_QE + qs, rq.phase() ^ 1))) break;
+      mbar_expect_tx(bar + 8 * (C::B_QF + qs), q_bytes);
+      load_tile<D>(sbase + C::Q_OFF + qs * C::TILE, &m.q, i * p.toks, w.hk, w.b, bar + 8 * (C::B_QF + qs));
+      ++rq.n;
+      if (i == w.q0) {
+        if (!(ok = wait(C::B_VE, rv.phase() ^ 1))) break;
+        mbar_expect_tx(bar + 8 * C::B_VF, C::TILE);
+        load_tile<D>(sbase + C::V_OFF, &m.v, w.kt * 128, w.hk, w.b, bar + 8 * C::B_VF);
+        ++rv.n;
+      }
+      if (!(ok = wait(C::B_OE + os, ro.phase() ^ 1))) break;
+      mbar_expect_tx(bar + 8 * (C::B_OF + os), q_bytes);
+      load_tile<D>(sbase + C::DO_OFF + os * C::TILE, &m.d_o, i * p.toks, w.hk, w.b, bar + 8 * (C::B_OF + os));
+      ++ro.n;
+    }
+  }
+  if (!ok) {
+    drain_ring(wait, C::B_KF, rk);
+    drain_ring(wait, C::B_VF, rv);
+    drain_ring(wait, C::B_QF, rq);
+    drain_ring(wait, C::B_OF, ro);
+  }
+}
+
+template <int D>
+__device__ void dkv_rows(const CrossParams& p, float* aux, const Waiter& wait) {
+  using C = CfgK<D>;
+  const int lane = threadIdx.x & 31;
+  Ring<C::NA> ra;
+  for (int it = blockIdx.x; it < p.total; it += gridDim.x) {
+    const ItemK w(p, it);
+    for (int i = w.q0; i < w.q1; ++i, ++ra.n) {
+      float nl[4], nd[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int r = lane + 32 * k, tr = r / p.group, tok = i * p.toks + tr, h = w.hk * p.group + r - tr * p.group;
+        nl[k] = neg_inf();
+        nd[k] = 0.f;
+        if (tr < p.toks && tok < p.nq) {
+          const int64_t row = ((int64_t)w.b * p.heads + h) * p.nq + tok;
+          nl[k] = neg_lse2(__ldg(p.lse + row));
+          nd[k] = -__ldg(p.delta + row);
+        }
+      }
+      if (!wait.warp(C::B_XE + ra.slot(), ra.phase() ^ 1)) return;
+      float* a = aux + ra.slot() * 256;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        a[lane + 32 * k] = nl[k];
+        a[128 + lane + 32 * k] = nd[k];
+      }
+      warp_arrive(wait.bar + 8 * (C::B_XF + ra.slot()));
+    }
+  }
+}
+
+template <typename T, int D>
+__device__ void dkv_mma(const CrossParams& p, uint32_t sbase, uint32_t tbase, const Waiter& wait) {
+  using C = CfgK<D>;
+  const uint32_t bar = wait.bar, tV = tbase + 256, tK = tbase + 256 + D;
+  Ring<1> rk;
+  Ring<C::NQ> rq;
+  Ring<C::NO> ro;
+  uint32_t g = 0, items = 0;
+  bool ok = true, pending = false, pfirst = false, plast = false;
+  uint32_t pslot = 0;
+  // dK += dS^T Q of step g - 1
+  auto accumulate = [&]() {
+    if (!wait(C::B_DS, (g - 1) & 1)) return false;
+    tc_fence_after();
+    mma_accum<T, D>(tK, tbase + 128, sbase + C::Q_OFF + pslot * C::TILE, pfirst);
+    mma_commit(bar + 8 * (C::B_QE + pslot));
+    if (plast) mma_commit(bar + 8 * C::B_AF);
+    return true;
+  };
+  for (int it = blockIdx.x; ok && it < p.total; it += gridDim.x) {
+    const ItemK w(p, it);
+    for (int i = w.q0; i < w.q1; ++i) {
+      const bool first = i == w.q0, last = i == w.q1 - 1;
+      if (first && !(ok = wait(C::B_KF, rk.phase()))) break;
+      if (!(ok = wait(C::B_QF + rq.slot(), rq.phase()))) break;
+      tc_fence_after();
+      // (overwrites P^T of step g - 1, which the product issued before has read)
+      mma_scores<T, D>(tbase, sbase, sbase + C::Q_OFF + rq.slot() * C::TILE);
+      mma_commit(bar + 8 * C::B_SF);
+      if (last) mma_commit(bar + 8 * C::B_KE);
+      if (pending && !(ok = accumulate())) break;
+      if (first && !(ok = wait(C::B_VF, rk.phase()))) break;
+      if (!(ok = wait(C::B_OF + ro.slot(), ro.phase()))) break;
+      tc_fence_after();
+      mma_scores<T, D>(tbase + 128, sbase + C::V_OFF, sbase + C::DO_OFF + ro.slot() * C::TILE);
+      mma_commit(bar + 8 * C::B_PF);
+      if (last) mma_commit(bar + 8 * C::B_VE);
+      if (!(ok = wait(C::B_PS, g & 1))) break;
+      if (first && items > 0 && !(ok = wait(C::B_AE, (items - 1) & 1))) break;
+      tc_fence_after();
+      mma_accum<T, D>(tV, tbase, sbase + C::DO_OFF + ro.slot() * C::TILE, first);
+      mma_commit(bar + 8 * (C::B_OE + ro.slot()));
+      pending = true;
+      pfirst = first;
+      plast = last;
+      pslot = rq.slot();
+      ++rq.n;
+      ++ro.n;
+      ++g;
+    }
+    if (w.q1 > w.q0) {
+      ++rk.n;
+      ++items;
+    }
+  }
+  if (ok && pending) ok = accumulate();
+  if (!ok) {
+    mma_commit(bar + 8 * C::B_DRAIN);
+    wait.drain(C::B_DRAIN, 0);
+  }
+}
+
+template <typename T, int D>
+__device__ void dkv_elementwise(const CrossParams& p, const float* aux, uint32_t tbase, const Waiter& wait) {
+  using C = CfgK<D>;
+  const uint32_t bar = wait.bar;
+  const int half = threadIdx.x >> 7, r = threadIdx.x & 127;
+  const uint32_t lane_off = (uint32_t)((threadIdx.x >> 5) & 3) * 32u << 16;
+  const uint32_t tS = tbase + lane_off + half * 64, tP = tS + 128, tAcc = tbase + lane_off + 256 + half * (D / 2);
+  const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
+  uint32_t g = 0, items = 0;
+  Ring<C::NA> ra;
+  T *pend_k = nullptr, *pend_v = nullptr;
+  float* pend_part = nullptr;
+  bool pending = false, pend_vis = false;
+  // the accumulators of the item before: dV, dK rows, or their fp32 partials [2][128][D]
+  auto finish = [&]() {
+    if (!wait.warp(C::B_AF, (items - 1) & 1)) return false;
+    tc_fence_after();
+    if (p.part) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int ch = 0; ch < D / 64; ++ch) {
+          uint32_t o[32];
+          __syncwarp();
+          tmem_ld32_sync(tAcc + t * D + ch * 32, o);
+          if (!pend_vis) continue;
+          uint4* dst = reinterpret_cast<uint4*>(pend_part + t * 128 * D + ch * 32);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) dst[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+        }
+    } else {
+      store_half<T, D>(tAcc, pend_v, 1.0f, pend_vis);
+      store_half<T, D>(tAcc + D, pend_k, p.scale, pend_vis);
+    }
+    tc_fence_before();
+    warp_arrive(bar + 8 * C::B_AE);
+    pending = false;
+    return true;
+  };
+  for (int it = blockIdx.x; it < p.total; it += gridDim.x) {
+    const ItemK w(p, it);
+    const int key = w.kt * 128 + r;
+    const uint4 words = cross_words(p, w.b, w.kt, w.len);
+    const bool vis = (word_of(words, r >> 5) >> (r & 31)) & 1u;
+    T* out_k = static_cast<T*>(p.out[0]) + w.b * p.out_st[0][0] + key * p.out_st[0][1] + w.hk * p.out_st[0][2] + half * (D / 2);
+    T* out_v = static_cast<T*>(p.out[1]) + w.b * p.out_st[1][0] + key * p.out_st[1][1] + w.hk * p.out_st[1][2] + half * (D / 2);
+    if (!p.part && key < p.ns && !vis) {       // (with partials the join writes these)
+      zero_half<T, D>(out_k);
+      zero_half<T, D>(out_v);
+    }
+    if (w.q1 == w.q0) continue;
+    const bool zero = w.len == 1 || (p.single && __ldg(p.single + w.b));
+    for (int i = w.q0; i < w.q1; ++i) {
+      uint32_t s[64];
+      const float4* nl = reinterpret_cast<const float4*>(aux + ra.slot() * 256 + half * 64);
+      if (!wait.warp(C::B_XF + ra.slot(), ra.phase())) return;
+      if (!wait.warp(C::B_SF, g & 1)) return;
+      tc_fence_after();
+      tmem_ld64_sync(tS, s);
+      uint32_t pk[32];
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        const float4 l = nl[c];
+        const float2 a = ffma2(make_float2(__uint_as_float(s[4 * c]), __uint_as_float(s[4 * c + 1])), scale2, make_float2(l.x, l.y));
+        const float2 b = ffma2(make_float2(__uint_as_float(s[4 * c + 2]), __uint_as_float(s[4 * c + 3])), scale2, make_float2(l.z, l.w));
+        s[4 * c] = __float_as_uint(ex2(a.x));
+        s[4 * c + 1] = __float_as_uint(ex2(a.y));
+        s[4 * c + 2] = __float_as_uint(ex2(b.x));
+        s[4 * c + 3] = __float_as_uint(ex2(b.y));
+        pk[2 * c] = vis ? pack2<T>(__uint_as_float(s[4 * c]), __uint_as_float(s[4 * c + 1])) : 0u;
+        pk[2 * c + 1] = vis ? pack2<T>(__uint_as_float(s[4 * c + 2]), __uint_as_float(s[4 * c + 3])) : 0u;
+      }
+      __syncwarp();
+      tmem_st32(tS, pk);
+      tmem_wait_st();
+      tc_fence_before();
+      warp_arrive(bar + 8 * C::B_PS);
+      if (!wait.warp(C::B_PF, g & 1)) return;
+      tc_fence_after();
+      const float4* nd = nl + 32;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t d[32];
+        tmem_ld32_sync(tP + h * 32, d);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const float4 l = nd[h * 8 + c];
+          const int k = h * 32 + 4 * c;
+          const float2 a = fmul2(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])),
+                                 fadd2(make_float2(__uint_as_float(d[4 * c]), __uint_as_float(d[4 * c + 1])), make_float2(l.x, l.y)));
+          const float2 b = fmul2(make_float2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])),
+                                 fadd2(make_float2(__uint_as_float(d[4 * c + 2]), __uint_as_float(d[4 * c + 3])), make_float2(l.z, l.w)));
+          pk[h * 16 + 2 * c] = vis && !zero ? pack2<T>(a.x, a.y) : 0u;
+          pk[h * 16 + 2 * c + 1] = vis && !zero ? pack2<T>(b.x, b.y) : 0u;
+        }
+      }
+      __syncwarp();
+      tmem_st32(tP, pk);
+      tmem_wait_st();
+      tc_fence_before();
+      warp_arrive(bar + 8 * C::B_DS);
+      warp_arrive(bar + 8 * (C::B_XE + ra.slot()));
+      ++ra.n;
+      ++g;
+      if (pending && !finish()) return;
+    }
+    ++items;
+    pending = true;
+    pend_k = out_k;
+    pend_v = out_v;
+    pend_vis = vis;
+    if (p.part) pend_part = p.part + ((int64_t)it * 2 * 128 + r) * D + half * (D / 2);
+  }
+  if (pending) finish();
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreadsK, 1) cross_dkv_kernel(const __grid_constant__ CrossMaps m, const CrossParams p) {
+  using C = CfgK<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  if (sbase & 1023) {
+    if (threadIdx.x == 0) atomicExch(&g_error, (int)DEV_TIMEOUT_PRODUCER);
+    return;
+  }
+  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
+  const uint32_t bar = sbase + C::BAR_OFF;
+  float* aux = reinterpret_cast<float*>(smem + C::AUX_OFF);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::NBAR; ++i) mbar_init(bar + 8 * i, C::arrivals(i));
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (p.toks * p.group < 128) {
+    uint4* q = reinterpret_cast<uint4*>(smem + C::Q_OFF);
+    for (int i = threadIdx.x; i < (C::NQ + C::NO) * C::TILE / 16; i += kThreadsK) q[i] = make_uint4(0, 0, 0, 0);
+    fence_async_smem();
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(smem_u32(misc), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = misc[0];
+  Waiter wait{bar, abort_flag, DEV_TIMEOUT_SOFTMAX, p.timeout_ns};
+  if (warp >= 8) {
+    regs_shrink<kRegsOtherK>();
+    if (warp == kWarpProducer) {
+      wait.code = DEV_TIMEOUT_PRODUCER;
+      if (lane == 0) dkv_producer<D>(m, p, sbase, wait);
+    } else if (warp == kWarpMma) {
+      wait.code = DEV_TIMEOUT_MMA;
+      if (lane == 0) dkv_mma<T, D>(p, sbase, tbase, wait);
+    } else if (warp == kWarpAux) {
+      dkv_rows<D>(p, aux, wait);
+    }
+  } else {
+    regs_grow<kRegsElemK>();
+    dkv_elementwise<T, D>(p, aux, tbase, wait);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kWarpMma) {
+    __syncwarp();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+// dK and dV of every key from the splits' partials, added in split order (nsplit = 0: no queries,
+// zeros).  One warp per key and tensor.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) cross_dkv_join_kernel(const CrossParams p) {
+  const int64_t r = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) >> 1;
+  const int t = (threadIdx.x >> 5) & 1, lane = threadIdx.x & 31;     // t: 0 dV, 1 dK
+  if (r >= (int64_t)p.units * p.ns) return;
+  const int key = (int)(r % p.ns), u = (int)(r / p.ns), b = u / p.kv_heads, hk = u - b * p.kv_heads;
+  const int nkt = (p.ns + 127) >> 7, kt = key >> 7;
+  const uint4 words = cross_words(p, b, kt, cross_len(p, b));
+  const bool vis = (word_of(words, (key >> 5) & 3) >> (key & 31)) & 1u;
+  float s[D / 32] = {};
+  if (vis)
+    for (int i = 0; i < p.nsplit; ++i) {
+      float v[D / 32];
+      load_f32<float, D / 32>(p.part + ((((int64_t)u * p.nsplit + i) * nkt + kt) * 256 + t * 128 + (key & 127)) * D + lane * (D / 32), v);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) s[c] += v[c];
+    }
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) s[c] *= t ? p.scale : 1.0f;
+  const int o = t ? 0 : 1;
+  store_f32<T, D / 32>(static_cast<T*>(p.out[o]) + b * p.out_st[o][0] + key * p.out_st[o][1] + hk * p.out_st[o][2] + lane * (D / 32), s);
+}
+
+// Launches `kernel`, whose register split is sound only if it has `regs` registers at launch.
+template <typename Tag, typename K>
+cudaError_t launch(K kernel, int regs, int threads, int smem, const CrossMaps& m, const CrossParams& p, int grid, cudaStream_t s) {
+  constexpr int kMaxDev = 64;
+  static std::mutex mu;
+  static bool attr_set[kMaxDev] = {};
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDev) return cudaErrorInvalidDevice;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!attr_set[dev]) {
+      cudaFuncAttributes fa;
+      if ((e = cudaFuncGetAttributes(&fa, kernel)) != cudaSuccess) return e;
+      if (fa.numRegs != regs) return cudaErrorInvalidConfiguration;
+      if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+      attr_set[dev] = true;
+    }
+  }
+  kernel<<<grid, threads, smem, s>>>(m, p);
+  return cudaGetLastError();
+}
+
+template <typename T, int D> struct TagQ {};
+template <typename T, int D> struct TagK {};
+
+template <typename T, int D>
+cudaError_t launch_dq(const CrossMaps& m, const CrossParams& p, int grid, cudaStream_t s) {
+  return launch<TagQ<T, D>>(cross_dq_kernel<T, D>, kRegsLaunchQ, kThreadsQ, CfgQ<D>::SMEM, m, p, grid, s);
+}
+template <typename T, int D>
+cudaError_t launch_dkv(const CrossMaps& m, const CrossParams& p, int grid, cudaStream_t s) {
+  if (p.total > 0) {
+    const cudaError_t e = launch<TagK<T, D>>(cross_dkv_kernel<T, D>, kRegsLaunchK, kThreadsK, CfgK<D>::SMEM, m, p, grid, s);
+    if (e != cudaSuccess || p.nsplit == 1) return e;
+  }
+  cross_dkv_join_kernel<T, D><<<(unsigned)(((int64_t)p.units * p.ns * 2 + 7) / 8), 256, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cross_dq(const CrossMaps& m, const CrossParams& p, int dtype, int D, int grid, cudaStream_t s) {
+  if (dtype == 0) return D == 128 ? launch_dq<__nv_bfloat16, 128>(m, p, grid, s) : launch_dq<__nv_bfloat16, 64>(m, p, grid, s);
+  return D == 128 ? launch_dq<__half, 128>(m, p, grid, s) : launch_dq<__half, 64>(m, p, grid, s);
+}
+
+cudaError_t launch_cross_dkv(const CrossMaps& m, const CrossParams& p, int dtype, int D, int grid, cudaStream_t s) {
+  if (dtype == 0) return D == 128 ? launch_dkv<__nv_bfloat16, 128>(m, p, grid, s) : launch_dkv<__nv_bfloat16, 64>(m, p, grid, s);
+  return D == 128 ? launch_dkv<__half, 128>(m, p, grid, s) : launch_dkv<__half, 64>(m, p, grid, s);
+}
+
+cudaError_t cross_bwd_status(int* code, cudaStream_t s) { return read_clear_error(&g_error, code, s); }
+
+}  // namespace ug

@@ -478,15 +478,6 @@ cudaError_t launch_cross_fwd(const CrossMaps& m, const CrossParams& p, int dtype
   return D == 128 ? launch<__half, 128>(m, p, grid, s) : launch<__half, 64>(m, p, grid, s);
 }
 
-cudaError_t cross_fwd_status(int* code, cudaStream_t s) {
-  const int zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbolAsync(code, g_error, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e == cudaSuccess && *code) {
-    e = cudaMemcpyToSymbolAsync(g_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  }
-  return e;
-}
+cudaError_t cross_fwd_status(int* code, cudaStream_t s) { return read_clear_error(&g_error, code, s); }
 
 }  // namespace ug
