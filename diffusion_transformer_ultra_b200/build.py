@@ -23,7 +23,7 @@ LIB = os.path.join(HERE, "libultragen.so")
 DEBUG_LIB = os.path.join(HERE, "libultragen_debug.so")
 
 SOURCES = ["plan.cpp", "api.cu", "permute.cu", "hla_fwd.cu", "noalloc.cu", "warm_start.cu", "host_runner.cu",
-           "layer_norm.cu", "adapter.cu", "cross_attention.cu", "cross_fwd.cu", "cross_bwd.cu"]
+           "layer_norm.cu", "adapter.cu", "adapter_gemm.cu", "cross_attention.cu", "cross_fwd.cu", "cross_bwd.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

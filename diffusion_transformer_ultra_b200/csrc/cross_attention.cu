@@ -13,6 +13,7 @@
 #include <cstdint>
 #include <cstring>
 
+#include "adapter.h"
 #include "cross.cuh"
 #include "device.h"
 #include "elem.cuh"
@@ -296,7 +297,9 @@ int ultragen_operator_status(ultragen_stream_t stream) {
   int back = 0;
   if ((st = status_of(cross_fwd_status(&code, reinterpret_cast<cudaStream_t>(stream))))) return st;
   if ((st = status_of(cross_bwd_status(&back, reinterpret_cast<cudaStream_t>(stream))))) return st;
-  return code || back ? ULTRAGEN_ERR_TIMEOUT : ULTRAGEN_OK;
+  int proj = 0;
+  if ((st = status_of(adapter_status(&proj, reinterpret_cast<cudaStream_t>(stream))))) return st;
+  return code || back || proj ? ULTRAGEN_ERR_TIMEOUT : ULTRAGEN_OK;
 }
 
 int ultragen_cross_attention_backward(const ultragen_cross_t* c, const void* d_o, const void* q, const void* k,
