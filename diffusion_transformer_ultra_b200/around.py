@@ -27,7 +27,7 @@ def _tensor(t, name, dtypes, shape=None, device=None):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} has dtype {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
@@ -40,6 +40,8 @@ def _contiguous(t, name, dtypes, shape, device):
 def _rows_apart(t, name, out=False):
     """Checks that the last dimension is contiguous and (for an output) that no two elements
     share memory."""
+    if t.is_contiguous():
+        return
     if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
     if out and t.numel():
@@ -64,12 +66,15 @@ def _other(device, stream):
                 yield
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _on(device, stream):
     """Makes `device`, and `stream` if given, current for the call."""
     if stream is not None and stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
     if stream is None and torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
+        return _HERE
     return _other(device, stream)
 
 
@@ -80,7 +85,7 @@ def _workspace(what, device, query, *args):
 
 
 def _stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def operator_status(stream=None) -> int:
