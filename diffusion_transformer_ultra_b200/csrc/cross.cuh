@@ -54,11 +54,49 @@ __device__ __forceinline__ uint32_t word_of(const uint4& w, int i) {
 }
 __device__ __forceinline__ bool all_visible(const uint4& w) { return (w.x & w.y & w.z & w.w) == ~0u; }
 
-// Key tiles [k0, k1) of split s of a sample with `len` visible keys.
+// Key tiles [k0, k1) of split s of a sample with `len` visible keys.  (At most 2^24 tiles and 64
+// splits: 32 bits hold the products.)
 __device__ __forceinline__ void split_range(int len, int s, int nsplit, int& k0, int& k1) {
-  const int n = (len + 127) >> 7;
-  k0 = (int)((int64_t)n * s / nsplit);
-  k1 = (int)((int64_t)n * (s + 1) / nsplit);
+  const uint32_t n = (len + 127) >> 7;
+  if (nsplit == 1) {
+    k0 = 0;
+    k1 = n;
+  } else {
+    k0 = n * s / (uint32_t)nsplit;
+    k1 = n * (s + 1) / (uint32_t)nsplit;
+  }
+}
+
+// Rows of a warp's accumulator (lane = row), scaled and rounded, to 16-bit global memory.  A lane's
+// row is one piece, but 32 lanes' 16-byte stores to 32 rows go one by one: the 64-column chunks pass
+// through 4 KB of the warp's shared memory and leave as whole 128-byte pieces, 8 lanes each.
+// `row` is the lane's row, null for one that is not stored.
+template <typename T, int COLS>
+__device__ __forceinline__ void store_rows(uint32_t tmem, uint8_t* stage, T* row, float f) {
+  const int lane = threadIdx.x & 31, c = lane & 7;
+#pragma unroll 1
+  for (int ch = 0; ch < COLS / 64; ++ch) {
+    uint32_t o[64];
+    __syncwarp();
+    tmem_ld64_sync(tmem + ch * 64, o);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      uint4 v;
+      v.x = pack2<T>(__uint_as_float(o[8 * q + 0]) * f, __uint_as_float(o[8 * q + 1]) * f);
+      v.y = pack2<T>(__uint_as_float(o[8 * q + 2]) * f, __uint_as_float(o[8 * q + 3]) * f);
+      v.z = pack2<T>(__uint_as_float(o[8 * q + 4]) * f, __uint_as_float(o[8 * q + 5]) * f);
+      v.w = pack2<T>(__uint_as_float(o[8 * q + 6]) * f, __uint_as_float(o[8 * q + 7]) * f);
+      *reinterpret_cast<uint4*>(stage + lane * 128 + ((q ^ (lane & 7)) * 16)) = v;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = i * 4 + (lane >> 3);
+      const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((c ^ (r & 7)) * 16));
+      T* dst = reinterpret_cast<T*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), r));
+      if (dst) *reinterpret_cast<uint4*>(dst + ch * 64 + c * 8) = v;
+    }
+  }
 }
 
 // Zeroes the rows of hidden keys of a [rows x D] tile in shared memory (rows of 128 bytes in

@@ -40,7 +40,7 @@ struct CrossParams {
 };
 
 struct CrossMaps {
-  CUtensorMap q, k, v, d_o;
+  CUtensorMap q, k, v, d_o, o;
 };
 
 // Keys [0, len) of sample b may be visible.

@@ -336,7 +336,8 @@ int ultragen_cross_attention_backward(const ultragen_cross_t* c, const void* d_o
   std::memset(&m, 0, sizeof(m));
   if (c->nq > 0 &&
       ((st = make_map(&m.q, q, sd[0], c->dtype, c->batch, c->nq, c->kv_heads, p.group, c->head_dim, p.toks)) ||
-       (st = make_map(&m.d_o, d_o, sd[4], c->dtype, c->batch, c->nq, c->kv_heads, p.group, c->head_dim, p.toks))))
+       (st = make_map(&m.d_o, d_o, sd[4], c->dtype, c->batch, c->nq, c->kv_heads, p.group, c->head_dim, p.toks)) ||
+       (st = make_map(&m.o, o, sd[3], c->dtype, c->batch, c->nq, c->kv_heads, p.group, c->head_dim, p.toks))))
     return st;
   if (c->ns > 0 &&
       ((st = make_map(&m.k, k, sd[1], c->dtype, c->batch, c->ns, c->kv_heads, 1, c->head_dim, 128)) ||

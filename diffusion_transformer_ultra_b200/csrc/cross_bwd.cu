@@ -79,7 +79,7 @@ __device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b) {
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk) {
     const uint32_t off = ((kk / 4) * BOX_BYTES + (kk % 4) * 32) >> 4;
-    mma_ss_w(d, alo + off, blo + off, desc_hi_sw128(1024), idesc_half<T>(128, 128, 0), kk > 0 ? 1u : 0u);
+    mma_ss_elect(d, alo + off, blo + off, desc_hi_sw128(1024), idesc_half<T>(128, 128, 0), kk > 0 ? 1u : 0u);
   }
 }
 
@@ -90,7 +90,7 @@ __device__ __forceinline__ void mma_accum(uint32_t d, uint32_t a, uint32_t b, bo
   const uint32_t blo = desc_lo(b, BOX_BYTES);
 #pragma unroll
   for (int kk = 0; kk < 8; ++kk)
-    mma_ts_w(d, a + (kk / 4) * 64 + (kk % 4) * 8, blo + kk * (2048 >> 4), desc_hi_sw128(1024), idesc_half<T>(128, D, 1),
+    mma_ts_elect(d, a + (kk / 4) * 64 + (kk % 4) * 8, blo + kk * (2048 >> 4), desc_hi_sw128(1024), idesc_half<T>(128, D, 1),
              (first && kk == 0) ? 0u : 1u);
 }
 
@@ -157,8 +157,8 @@ static_assert(256 * kRegsElemQ + 256 * kRegsOtherQ <= kThreadsQ * kRegsLaunchQ, 
 struct ItemQ {
   int b, hk, qt, len, n;
   __device__ __forceinline__ ItemQ(const CrossParams& p, int it) {
-    qt = it % p.nqt;
-    const int u = it / p.nqt;
+    const uint32_t u = (uint32_t)it / p.nqt;
+    qt = it - u * p.nqt;
     b = u / p.kv_heads;
     hk = u - b * p.kv_heads;
     len = cross_len(p, b);
@@ -177,6 +177,17 @@ __device__ void dq_producer(const CrossMaps& m, const CrossParams& p, uint32_t s
   bool ok = true;
   for (int it = blockIdx.x; ok && it < p.total; it += gridDim.x) {
     const ItemQ w(p, it);
+    const int ahead = it + 2 * (int)gridDim.x;
+    if (ahead < p.total) {             // (total + 2 grids stays below 2^31: see the entry point's check)
+      // the rows of the item after next into L2: delta reads them an item ahead of the products
+      const ItemQ a(p, ahead);
+#pragma unroll
+      for (int bx = 0; bx < D / 64; ++bx) {
+        tma_prefetch_5d(&m.o, bx * 64, 0, a.qt * p.toks, a.hk, a.b);
+        tma_prefetch_5d(&m.d_o, bx * 64, 0, a.qt * p.toks, a.hk, a.b);
+        tma_prefetch_5d(&m.q, bx * 64, 0, a.qt * p.toks, a.hk, a.b);
+      }
+    }
     for (int j = 0; j < w.n; ++j) {
       if (j == 0) {
         if (!(ok = wait(C::B_QE, rq.phase() ^ 1))) break;
@@ -286,50 +297,50 @@ __device__ void dq_mma(const CrossParams& p, uint32_t sbase, uint32_t tbase, con
   uint32_t pslot = 0, pitem = 0;
   // dQ += dS K of step g - 1
   auto accumulate = [&]() {
-    if (!wait(C::B_DS, (g - 1) & 1)) return false;
-    if (pfirst && pitem > 0 && !wait(C::B_AE, (pitem - 1) & 1)) return false;
+    if (!wait.warp(C::B_DS, (g - 1) & 1)) return false;
+    if (pfirst && pitem > 0 && !wait.warp(C::B_AE, (pitem - 1) & 1)) return false;
     tc_fence_after();
     mma_accum<T, D>(tAcc, tbase + 128 + 128 * ((g - 1) & 1), sbase + C::K_OFF + pslot * C::TILE, pfirst);
-    mma_commit(bar + 8 * (C::B_KE + pslot));
-    if (plast) mma_commit(bar + 8 * C::B_AF);
+    mma_commit_elect(bar + 8 * (C::B_KE + pslot));
+    if (plast) mma_commit_elect(bar + 8 * C::B_AF);
     return true;
   };
   for (int it = blockIdx.x; ok && it < p.total; it += gridDim.x) {
-    const ItemQ w(p, it);
-    for (int j = 0; j < w.n; ++j) {
-      if (j == 0 && !(ok = wait(C::B_QF, rq.phase()))) break;
-      if (!(ok = wait(kready + rk.slot(), rk.phase()))) break;
-      if (g > 0 && !(ok = wait(C::B_SR, (g - 1) & 1))) break;
+    const int n = uniform(ItemQ(p, it).n);
+    for (int j = 0; j < n; ++j) {
+      if (j == 0 && !(ok = wait.warp(C::B_QF, rq.phase()))) break;
+      if (!(ok = wait.warp(kready + rk.slot(), rk.phase()))) break;
+      if (g > 0 && !(ok = wait.warp(C::B_SR, (g - 1) & 1))) break;
       tc_fence_after();
       mma_scores<T, D>(tbase, sbase, sbase + C::K_OFF + rk.slot() * C::TILE);
-      mma_commit(bar + 8 * C::B_SF);
-      if (j == w.n - 1) mma_commit(bar + 8 * C::B_QE);
-      if (j == 0 && !(ok = wait(C::B_OF, rq.phase()))) break;
-      if (!(ok = wait(C::B_VF + rv.slot(), rv.phase()))) break;
+      mma_commit_elect(bar + 8 * C::B_SF);
+      if (j == n - 1) mma_commit_elect(bar + 8 * C::B_QE);
+      if (j == 0 && !(ok = wait.warp(C::B_OF, rq.phase()))) break;
+      if (!(ok = wait.warp(C::B_VF + rv.slot(), rv.phase()))) break;
       tc_fence_after();
       // (overwrites dS of step g - 2, which the product issued before has read)
       mma_scores<T, D>(tbase + 128 + 128 * (g & 1), sbase + C::DO_OFF, sbase + C::V_OFF + rv.slot() * C::TILE);
-      mma_commit(bar + 8 * (C::B_PF + (g & 1)));
-      mma_commit(bar + 8 * (C::B_VE + rv.slot()));
-      if (j == w.n - 1) mma_commit(bar + 8 * C::B_OE);
+      mma_commit_elect(bar + 8 * (C::B_PF + (g & 1)));
+      mma_commit_elect(bar + 8 * (C::B_VE + rv.slot()));
+      if (j == n - 1) mma_commit_elect(bar + 8 * C::B_OE);
       if (pending && !(ok = accumulate())) break;
       pending = true;
       pfirst = j == 0;
-      plast = j == w.n - 1;
+      plast = j == n - 1;
       pslot = rk.slot();
       pitem = items;
       ++rk.n;
       ++rv.n;
       ++g;
     }
-    if (w.n > 0) {
+    if (n > 0) {
       ++rq.n;
       ++items;
     }
   }
   if (ok && pending) ok = accumulate();
   if (!ok) {
-    mma_commit(bar + 8 * C::B_DRAIN);
+    mma_commit_elect(bar + 8 * C::B_DRAIN);
     wait.drain(C::B_DRAIN, 0);
   }
 }
@@ -345,6 +356,15 @@ __device__ void dq_elementwise(const CrossParams& p, float* red, uint32_t tbase,
   const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
   uint32_t g = 0, items = 0, xn = 0;
   Ring<2> rd;
+  // -lse log2(e) of this thread's row of item `it`, fetched an item ahead
+  auto row_constant = [&](int it) {
+    if (it >= p.total) return neg_inf();
+    const ItemQ w(p, it);
+    const int tok = w.qt * p.toks + tok_r;
+    if (tok_r >= p.toks || tok >= p.nq) return neg_inf();
+    return __ldg(p.lse + ((int64_t)w.b * p.heads + w.hk * p.group + g_r) * p.nq + tok);
+  };
+  float lse = row_constant(blockIdx.x);
   T* pend = nullptr;                   // dq row of the item whose accumulator is still to be read
   bool pending = false, pend_on = false;
   auto finish = [&]() {
@@ -363,11 +383,13 @@ __device__ void dq_elementwise(const CrossParams& p, float* red, uint32_t tbase,
     T* out = static_cast<T*>(p.out[0]) + w.b * p.out_st[0][0] + tok * p.out_st[0][1] + h * p.out_st[0][2] + half * (D / 2);
     if (w.n == 0) {
       if (real) zero_half<T, D>(out);
+      lse = row_constant(it + gridDim.x);
       continue;
     }
     const int64_t row = ((int64_t)w.b * p.heads + h) * p.nq + tok;
-    const float nl = real ? neg_lse2(__ldg(p.lse + row)) : neg_inf();
+    const float nl = neg_lse2(lse);
     const float2 nl2 = make_float2(nl, nl);
+    lse = row_constant(it + gridDim.x);
     // one visible key has weight one whatever its logit: dS is zero exactly
     const bool zero = w.len == 1 || (p.single && __ldg(p.single + w.b));
     float nd = 0.f;                    // -delta
@@ -457,7 +479,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1) cross_dq_kernel(const __grid_con
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
   const uint32_t bar = sbase + C::BAR_OFF;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NBAR; ++i) mbar_init(bar + 8 * i, C::arrivals(i));
     *abort_flag = 0;
@@ -484,7 +506,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1) cross_dq_kernel(const __grid_con
       if (lane == 0) dq_producer<D>(m, p, sbase, wait);
     } else if (warp == kWarpMma) {
       wait.code = DEV_TIMEOUT_MMA;
-      if (lane == 0) dq_mma<T, D>(p, sbase, tbase, wait);
+      dq_mma<T, D>(p, sbase, uniform(tbase), wait);
     } else if (warp == kWarpAux) {
       if (p.scrub) dq_scrub<D>(p, sbase, wait);
     } else if (warp >= 12) {
@@ -505,7 +527,11 @@ __global__ void __launch_bounds__(kThreadsQ, 1) cross_dq_kernel(const __grid_con
 
 // ---------------------------------------------------------------------------------- dK, dV
 // 384 threads: warp 10 brings each step's -lse log2(e) and -delta into shared memory.
-// TMEM: S^T / P^T [0,128), dP^T / dS^T [128,256), dV [256,256+D), dK [256+D,256+2D).
+// TMEM: S^T [0,128), dP^T [128,256), dV [256,256+D), dK [256+D,256+2D).  A warp that holds its dP^T
+// in registers writes P^T and dS^T (16 bits, 32 columns each) over it, so that S^T is free as soon
+// as it is read and the next S^T is made beside this step's exponentials.  (With P^T over S^T, a
+// step waits for its own dV product and the next S^T: 163 instead of 1XX us for the pass at
+// 4 x 4,096 queries x 512 keys x 24 heads of 128.)
 template <int D>
 struct CfgK {
   static constexpr int TILE = 128 * D * 2;
@@ -513,16 +539,16 @@ struct CfgK {
   static constexpr int V_OFF = TILE, Q_OFF = 2 * TILE, DO_OFF = Q_OFF + NQ * TILE;
   static constexpr int AUX_OFF = DO_OFF + NO * TILE;           // [NA][2][128] floats
   static constexpr int BAR_OFF = AUX_OFF + NA * 2 * 128 * 4;
-  // full / empty of K, V, Q, dO and the row constants; S ready; P stored; dP ready; dS stored;
+  // full / empty of K, V, Q, dO and the row constants; S ready / read; dP ready; P and dS stored;
   // accumulators ready / read
   static constexpr int B_KF = 0, B_KE = 1, B_VF = 2, B_VE = 3, B_QF = 4, B_QE = B_QF + NQ, B_OF = B_QE + NQ, B_OE = B_OF + NO,
-                       B_XF = B_OE + NO, B_XE = B_XF + NA, B_SF = B_XE + NA, B_PS = B_SF + 1, B_PF = B_PS + 1, B_DS = B_PF + 1,
+                       B_XF = B_OE + NO, B_XE = B_XF + NA, B_SF = B_XE + NA, B_SR = B_SF + 1, B_PF = B_SR + 1, B_DS = B_PF + 1,
                        B_AF = B_DS + 1, B_AE = B_AF + 1, B_DRAIN = B_AE + 1, NBAR = B_DRAIN + 1;
   static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
   static constexpr int SMEM = MISC_OFF + 16;
   static_assert(SMEM <= 227 * 1024, "shared memory per CTA exceeds 227 KB");
   static __device__ __forceinline__ uint32_t arrivals(int i) {
-    return i == B_PS || i == B_DS || i == B_AE || (i >= B_XE && i < B_XE + NA) ? 8 : 1;   // 8 elementwise warps
+    return i == B_SR || i == B_DS || i == B_AE || (i >= B_XE && i < B_XE + NA) ? 8 : 1;   // 8 elementwise warps
   }
 };
 constexpr int kThreadsK = 384, kRegsLaunchK = 168, kRegsElemK = 208, kRegsOtherK = 80;
@@ -533,16 +559,20 @@ static_assert(256 * kRegsElemK + 128 * kRegsOtherK <= kThreadsK * kRegsLaunchK, 
 struct ItemK {
   int b, hk, kt, split, len, q0, q1;
   __device__ __forceinline__ ItemK(const CrossParams& p, int it) {
-    const int nkt = (p.ns + 127) >> 7;
-    kt = it % nkt;
-    it /= nkt;
-    split = it % p.nsplit;
-    const int u = it / p.nsplit;
+    const uint32_t nkt = (p.ns + 127) >> 7;
+    uint32_t i = (uint32_t)it / nkt, u = i;
+    kt = it - i * nkt;
+    split = 0;
+    if (p.nsplit > 1) {
+      u = i / (uint32_t)p.nsplit;
+      split = i - u * p.nsplit;
+    }
     b = u / p.kv_heads;
     hk = u - b * p.kv_heads;
     len = cross_len(p, b);
-    q0 = (int)((int64_t)p.nqt * split / p.nsplit);
-    q1 = kt * 128 < len ? (int)((int64_t)p.nqt * (split + 1) / p.nsplit) : q0;
+    // (fewer than 2^24 query tiles, at most 64 splits: 32 bits hold the products)
+    q0 = split ? (uint32_t)p.nqt * split / (uint32_t)p.nsplit : 0;
+    q1 = kt * 128 < len ? (split + 1 < p.nsplit ? (uint32_t)p.nqt * (split + 1) / (uint32_t)p.nsplit : p.nqt) : q0;
   }
 };
 
@@ -630,55 +660,57 @@ __device__ void dkv_mma(const CrossParams& p, uint32_t sbase, uint32_t tbase, co
   Ring<C::NO> ro;
   uint32_t g = 0, items = 0;
   bool ok = true, pending = false, pfirst = false, plast = false;
-  uint32_t pslot = 0;
-  // dK += dS^T Q of step g - 1
+  uint32_t pq = 0, po = 0, pitem = 0;
+  // dV += P^T dO and dK += dS^T Q of step g - 1
   auto accumulate = [&]() {
-    if (!wait(C::B_DS, (g - 1) & 1)) return false;
+    if (!wait.warp(C::B_DS, (g - 1) & 1)) return false;
+    if (pfirst && pitem > 0 && !wait.warp(C::B_AE, (pitem - 1) & 1)) return false;
     tc_fence_after();
-    mma_accum<T, D>(tK, tbase + 128, sbase + C::Q_OFF + pslot * C::TILE, pfirst);
-    mma_commit(bar + 8 * (C::B_QE + pslot));
-    if (plast) mma_commit(bar + 8 * C::B_AF);
+    mma_accum<T, D>(tV, tbase + 128, sbase + C::DO_OFF + po * C::TILE, pfirst);
+    mma_commit_elect(bar + 8 * (C::B_OE + po));
+    mma_accum<T, D>(tK, tbase + 160, sbase + C::Q_OFF + pq * C::TILE, pfirst);
+    mma_commit_elect(bar + 8 * (C::B_QE + pq));
+    if (plast) mma_commit_elect(bar + 8 * C::B_AF);
     return true;
   };
   for (int it = blockIdx.x; ok && it < p.total; it += gridDim.x) {
     const ItemK w(p, it);
-    for (int i = w.q0; i < w.q1; ++i) {
-      const bool first = i == w.q0, last = i == w.q1 - 1;
-      if (first && !(ok = wait(C::B_KF, rk.phase()))) break;
-      if (!(ok = wait(C::B_QF + rq.slot(), rq.phase()))) break;
+    const int q0 = uniform(w.q0), q1 = uniform(w.q1);
+    for (int i = q0; i < q1; ++i) {
+      const bool first = i == q0, last = i == q1 - 1;
+      if (first && !(ok = wait.warp(C::B_KF, rk.phase()))) break;
+      if (!(ok = wait.warp(C::B_QF + rq.slot(), rq.phase()))) break;
+      if (g > 0 && !(ok = wait.warp(C::B_SR, (g - 1) & 1))) break;
       tc_fence_after();
-      // (overwrites P^T of step g - 1, which the product issued before has read)
       mma_scores<T, D>(tbase, sbase, sbase + C::Q_OFF + rq.slot() * C::TILE);
-      mma_commit(bar + 8 * C::B_SF);
-      if (last) mma_commit(bar + 8 * C::B_KE);
+      mma_commit_elect(bar + 8 * C::B_SF);
+      if (last) mma_commit_elect(bar + 8 * C::B_KE);
       if (pending && !(ok = accumulate())) break;
-      if (first && !(ok = wait(C::B_VF, rk.phase()))) break;
-      if (!(ok = wait(C::B_OF + ro.slot(), ro.phase()))) break;
+      if (first && !(ok = wait.warp(C::B_VF, rk.phase()))) break;
+      if (!(ok = wait.warp(C::B_OF + ro.slot(), ro.phase()))) break;
       tc_fence_after();
+      // (overwrites P^T and dS^T of step g - 1, which the products issued before have read)
       mma_scores<T, D>(tbase + 128, sbase + C::V_OFF, sbase + C::DO_OFF + ro.slot() * C::TILE);
-      mma_commit(bar + 8 * C::B_PF);
-      if (last) mma_commit(bar + 8 * C::B_VE);
-      if (!(ok = wait(C::B_PS, g & 1))) break;
-      if (first && items > 0 && !(ok = wait(C::B_AE, (items - 1) & 1))) break;
-      tc_fence_after();
-      mma_accum<T, D>(tV, tbase, sbase + C::DO_OFF + ro.slot() * C::TILE, first);
-      mma_commit(bar + 8 * (C::B_OE + ro.slot()));
+      mma_commit_elect(bar + 8 * C::B_PF);
+      if (last) mma_commit_elect(bar + 8 * C::B_VE);
       pending = true;
       pfirst = first;
       plast = last;
-      pslot = rq.slot();
+      pq = rq.slot();
+      po = ro.slot();
+      pitem = items;
       ++rq.n;
       ++ro.n;
       ++g;
     }
-    if (w.q1 > w.q0) {
+    if (q1 > q0) {
       ++rk.n;
       ++items;
     }
   }
   if (ok && pending) ok = accumulate();
   if (!ok) {
-    mma_commit(bar + 8 * C::B_DRAIN);
+    mma_commit_elect(bar + 8 * C::B_DRAIN);
     wait.drain(C::B_DRAIN, 0);
   }
 }
@@ -742,7 +774,9 @@ __device__ void dkv_elementwise(const CrossParams& p, const float* aux, uint32_t
       if (!wait.warp(C::B_SF, g & 1)) return;
       tc_fence_after();
       tmem_ld64_sync(tS, s);
-      uint32_t pk[32];
+      tc_fence_before();
+      warp_arrive(bar + 8 * C::B_SR);
+      uint32_t pk[32], dk[32];
 #pragma unroll
       for (int c = 0; c < 16; ++c) {
         const float4 l = nl[c];
@@ -755,32 +789,25 @@ __device__ void dkv_elementwise(const CrossParams& p, const float* aux, uint32_t
         pk[2 * c] = vis ? pack2<T>(__uint_as_float(s[4 * c]), __uint_as_float(s[4 * c + 1])) : 0u;
         pk[2 * c + 1] = vis ? pack2<T>(__uint_as_float(s[4 * c + 2]), __uint_as_float(s[4 * c + 3])) : 0u;
       }
-      __syncwarp();
-      tmem_st32(tS, pk);
-      tmem_wait_st();
-      tc_fence_before();
-      warp_arrive(bar + 8 * C::B_PS);
       if (!wait.warp(C::B_PF, g & 1)) return;
       tc_fence_after();
       const float4* nd = nl + 32;
+      uint32_t d[64];
+      tmem_ld64_sync(tP, d);
+      tmem_st32(tP, pk);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t d[32];
-        tmem_ld32_sync(tP + h * 32, d);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const float4 l = nd[h * 8 + c];
-          const int k = h * 32 + 4 * c;
-          const float2 a = fmul2(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])),
-                                 fadd2(make_float2(__uint_as_float(d[4 * c]), __uint_as_float(d[4 * c + 1])), make_float2(l.x, l.y)));
-          const float2 b = fmul2(make_float2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])),
-                                 fadd2(make_float2(__uint_as_float(d[4 * c + 2]), __uint_as_float(d[4 * c + 3])), make_float2(l.z, l.w)));
-          pk[h * 16 + 2 * c] = vis && !zero ? pack2<T>(a.x, a.y) : 0u;
-          pk[h * 16 + 2 * c + 1] = vis && !zero ? pack2<T>(b.x, b.y) : 0u;
-        }
+      for (int c = 0; c < 16; ++c) {
+        const float4 l = nd[c];
+        const int k = 4 * c;
+        const float2 a = fmul2(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])),
+                               fadd2(make_float2(__uint_as_float(d[k]), __uint_as_float(d[k + 1])), make_float2(l.x, l.y)));
+        const float2 b = fmul2(make_float2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])),
+                               fadd2(make_float2(__uint_as_float(d[k + 2]), __uint_as_float(d[k + 3])), make_float2(l.z, l.w)));
+        dk[2 * c] = vis && !zero ? pack2<T>(a.x, a.y) : 0u;
+        dk[2 * c + 1] = vis && !zero ? pack2<T>(b.x, b.y) : 0u;
       }
       __syncwarp();
-      tmem_st32(tP, pk);
+      tmem_st32(tP + 32, dk);
       tmem_wait_st();
       tc_fence_before();
       warp_arrive(bar + 8 * C::B_DS);
@@ -812,7 +839,7 @@ __global__ void __launch_bounds__(kThreadsK, 1) cross_dkv_kernel(const __grid_co
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
   const uint32_t bar = sbase + C::BAR_OFF;
   float* aux = reinterpret_cast<float*>(smem + C::AUX_OFF);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NBAR; ++i) mbar_init(bar + 8 * i, C::arrivals(i));
     *abort_flag = 0;
@@ -839,7 +866,7 @@ __global__ void __launch_bounds__(kThreadsK, 1) cross_dkv_kernel(const __grid_co
       if (lane == 0) dkv_producer<D>(m, p, sbase, wait);
     } else if (warp == kWarpMma) {
       wait.code = DEV_TIMEOUT_MMA;
-      if (lane == 0) dkv_mma<T, D>(p, sbase, tbase, wait);
+      dkv_mma<T, D>(p, sbase, uniform(tbase), wait);
     } else if (warp == kWarpAux) {
       dkv_rows<D>(p, aux, wait);
     }

@@ -28,7 +28,8 @@ struct Cfg {
   static constexpr int NS = D == 128 ? 4 : 8;      // tile slots
   static constexpr int NSTG = NS / 2;              // stages in flight (two tiles each)
   static constexpr int KV_OFF = 2 * TILE_BYTES;
-  static constexpr int BAR_OFF = KV_OFF + NS * TILE_BYTES;
+  static constexpr int OUT_OFF = KV_OFF + NS * TILE_BYTES;      // 8 warps x 32 rows x 128 bytes
+  static constexpr int BAR_OFF = OUT_OFF + 8 * 4096;
   // Q full / empty, stage full / scrubbed / empty, S ready, P ready, O ready (per query tile), drain
   static constexpr int B_QF = 0, B_QE = 1, B_KVF = 2, B_KVS = B_KVF + NSTG, B_KVE = B_KVS + NSTG,
                        B_SF = B_KVE + NSTG, B_PF = B_SF + 2, B_OF = B_PF + 2, B_DRAIN = B_OF + 2,
@@ -56,10 +57,14 @@ constexpr uint64_t kDrainNs = 50ull * 1000 * 1000;   // bounded drain on the abo
 struct Item {
   int b, hk, qt0, ntile, split, len, k0, k1;
   __device__ __forceinline__ Item(const CrossParams& p, int it) {
-    split = it % p.nsplit;
-    it /= p.nsplit;
-    qt0 = it % p.nitem_q * p.per_item;
-    const int u = it / p.nitem_q;
+    uint32_t i = it, u;
+    split = 0;
+    if (p.nsplit > 1) {
+      split = i % p.nsplit;
+      i /= p.nsplit;
+    }
+    u = i / p.nitem_q;
+    qt0 = (i - u * p.nitem_q) * p.per_item;
     b = u / p.kv_heads;
     hk = u - b * p.kv_heads;
     ntile = min(p.per_item, p.nqt - qt0);
@@ -152,11 +157,11 @@ __device__ void mma_role(const CrossParams& p, uint32_t sbase, uint32_t tbase, v
   uint32_t st = 0, qi = 0, pc[2] = {0, 0};
   bool ok = true;
   auto wait = [&](int b, uint32_t par) {
-    return mbar_wait(bar + 8 * b, par, abort_flag, &g_error, DEV_TIMEOUT_MMA, p.timeout_ns);
+    return __all_sync(0xffffffffu, mbar_wait(bar + 8 * b, par, abort_flag, &g_error, DEV_TIMEOUT_MMA, p.timeout_ns));
   };
   for (int it = blockIdx.x; ok && it < p.total; it += gridDim.x) {
     const Item w(p, it);
-    const int n = w.k1 - w.k0;
+    const int n = uniform(w.k1 - w.k0), ntile = uniform(w.ntile);
     if (n == 0) continue;
     if (!wait(C::B_QF, qi & 1)) { ok = false; break; }
     ++qi;
@@ -169,14 +174,14 @@ __device__ void mma_role(const CrossParams& p, uint32_t sbase, uint32_t tbase, v
       const uint32_t klo = desc_lo(sKV + C::k_slot(g) * C::TILE_BYTES, 16);
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        if (t >= w.ntile) break;
+        if (t >= ntile) break;
         if (j > 0) {
           if (!wait(C::B_PF + t, pc[t] & 1)) { ok = false; break; }
           ++pc[t];
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_ts_w(tbase + C::O_COL + D * t, tbase + 128 * t + kk * 8, vlo + kk * (2048 >> 4), hi, idO,
+            mma_ts_elect(tbase + C::O_COL + D * t, tbase + 128 * t + kk * 8, vlo + kk * (2048 >> 4), hi, idO,
                      (j > 1 || kk > 0) ? 1u : 0u);
         }
         if (j < n) {
@@ -184,21 +189,21 @@ __device__ void mma_role(const CrossParams& p, uint32_t sbase, uint32_t tbase, v
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = ((kk / 4) * C::BOX_BYTES + (kk % 4) * 32) >> 4;
-            mma_ss_w(tbase + 128 * t, qlo + off, klo + off, hi, idS, kk > 0 ? 1u : 0u);
+            mma_ss_elect(tbase + 128 * t, qlo + off, klo + off, hi, idS, kk > 0 ? 1u : 0u);
           }
-          mma_commit(bar + 8 * (C::B_SF + t));
+          mma_commit_elect(bar + 8 * (C::B_SF + t));
         } else {
-          mma_commit(bar + 8 * (C::B_OF + t));
+          mma_commit_elect(bar + 8 * (C::B_OF + t));
         }
       }
       if (!ok) break;
-      mma_commit(bar + 8 * (C::B_KVE + g));
-      if (j == n - 1) mma_commit(bar + 8 * C::B_QE);
+      mma_commit_elect(bar + 8 * (C::B_KVE + g));
+      if (j == n - 1) mma_commit_elect(bar + 8 * C::B_QE);
       ++st;
     }
   }
   if (!ok) {
-    mma_commit(bar + 8 * C::B_DRAIN);
+    mma_commit_elect(bar + 8 * C::B_DRAIN);
     mbar_wait(bar + 8 * C::B_DRAIN, 0, nullptr, &g_error, DEV_TIMEOUT_DRAIN, kDrainNs);
   }
 }
@@ -244,7 +249,7 @@ __device__ __forceinline__ void rescale_o(uint32_t tO, float f) {
 }
 
 template <typename T, int D>
-__device__ void softmax_role(const CrossParams& p, uint32_t sbase, uint32_t tbase, volatile int* abort_flag) {
+__device__ void softmax_role(const CrossParams& p, uint8_t* smem, uint32_t sbase, uint32_t tbase, volatile int* abort_flag) {
   using C = Cfg<D>;
   const uint32_t bar = sbase + C::BAR_OFF;
   const int t = threadIdx.x >> 7, r = threadIdx.x & 127;
@@ -253,6 +258,7 @@ __device__ void softmax_role(const CrossParams& p, uint32_t sbase, uint32_t tbas
   const uint32_t tO = tbase + lane_off + C::O_COL + (uint32_t)(t * D);
   const float scale = p.scale_log2;
   const int tok_r = r / p.group, g_r = r - tok_r * p.group;
+  uint8_t* out = smem + C::OUT_OFF + (threadIdx.x >> 5) * 4096;
   uint32_t sc = 0, oc = 0;
   for (int it = blockIdx.x; it < p.total; it += gridDim.x) {
     const Item w(p, it);
@@ -363,30 +369,22 @@ __device__ void softmax_role(const CrossParams& p, uint32_t sbase, uint32_t tbas
       }
       continue;
     }
+    // a row without a visible key has O = 0 products of P = 0: inv = 0 keeps it zero
+    if (p.part) {
 #pragma unroll
-    for (int ch = 0; ch < D / 32; ++ch) {
-      uint32_t o[32];
-      __syncwarp();
-      tmem_ld32_sync(tO + ch * 32, o);                 // warp-wide: every lane loads
-      // a row without a visible key has O = 0 products of P = 0: inv = 0 keeps it zero
-      if (orow) {
-        uint4* dst = reinterpret_cast<uint4*>(orow + ch * 32);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint4 v;
-          v.x = pack2<T>(__uint_as_float(o[8 * q + 0]) * inv, __uint_as_float(o[8 * q + 1]) * inv);
-          v.y = pack2<T>(__uint_as_float(o[8 * q + 2]) * inv, __uint_as_float(o[8 * q + 3]) * inv);
-          v.z = pack2<T>(__uint_as_float(o[8 * q + 4]) * inv, __uint_as_float(o[8 * q + 5]) * inv);
-          v.w = pack2<T>(__uint_as_float(o[8 * q + 6]) * inv, __uint_as_float(o[8 * q + 7]) * inv);
-          dst[q] = v;
-        }
-      } else if (prow) {
+      for (int ch = 0; ch < D / 32; ++ch) {
+        uint32_t o[32];
+        __syncwarp();
+        tmem_ld32_sync(tO + ch * 32, o);               // warp-wide: every lane loads
+        if (!prow) continue;
         float4* dst = reinterpret_cast<float4*>(prow + ch * 32);
 #pragma unroll
         for (int q = 0; q < 8; ++q)
           dst[q] = make_float4(__uint_as_float(o[4 * q + 0]) * inv, __uint_as_float(o[4 * q + 1]) * inv,
                                __uint_as_float(o[4 * q + 2]) * inv, __uint_as_float(o[4 * q + 3]) * inv);
       }
+    } else {
+      store_rows<T, D>(tO, out, orow, inv);
     }
     tc_fence_before();
   }
@@ -403,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t bar = sbase + C::BAR_OFF;
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NBAR; ++i)
       mbar_init(bar + 8 * i, i == C::B_PF || i == C::B_PF + 1 ? 4 : 1);   // P: one arrive per softmax warp
@@ -429,13 +427,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kWarpProducer) {
       if (lane == 0) producer_role<D>(m, p, sbase, abort_flag);
     } else if (warp == kWarpMma) {
-      if (lane == 0) mma_role<T, D>(p, sbase, tbase, abort_flag);
+      mma_role<T, D>(p, sbase, uniform(tbase), abort_flag);
     } else if (warp == kWarpScrub && p.scrub) {
       scrub_role<D>(p, sbase, abort_flag);
     }
   } else {
     regs_grow<kRegsSoftmax>();
-    softmax_role<T, D>(p, sbase, tbase, abort_flag);
+    softmax_role<T, D>(p, smem, sbase, tbase, abort_flag);
   }
   tc_fence_before();
   __syncthreads();
