@@ -94,25 +94,49 @@ __device__ __forceinline__ void mma_accum(uint32_t d, uint32_t a, uint32_t b, bo
              (first && kk == 0) ? 0u : 1u);
 }
 
-// Half a row of an accumulator, scaled and rounded, to 16-bit global memory.
+// Half a row of an accumulator per lane, scaled and rounded, to 16-bit global memory.  Stores by row
+// would go to 32 rows each; N = D / 16 lanes exchange their 16-byte pieces first (a transpose of N x N
+// pieces in log2(N) rounds), so that N lanes write one row's piece of 32 N / 2 bytes together.  `row`
+// is the lane's destination, null for a row that is not stored.
 template <typename T, int D>
-__device__ __forceinline__ void store_half(uint32_t tmem, T* dst, float f, bool on) {
-#pragma unroll
-  for (int ch = 0; ch < D / 64; ++ch) {
-    uint32_t o[32];
+__device__ __forceinline__ void store_half(uint32_t tmem, T* row, float f) {
+  constexpr int N = D / 16;
+  const int lane = threadIdx.x & 31, c = lane & (N - 1);
+  uint4 v[N];
+  {
+    uint32_t o[D / 2];
     __syncwarp();
-    tmem_ld32_sync(tmem + ch * 32, o);
-    if (!on) continue;
-    uint4* out = reinterpret_cast<uint4*>(dst + ch * 32);
+    if constexpr (D == 128) tmem_ld64_sync(tmem, o);
+    else tmem_ld32_sync(tmem, o);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint4 v;
-      v.x = pack2<T>(__uint_as_float(o[8 * q + 0]) * f, __uint_as_float(o[8 * q + 1]) * f);
-      v.y = pack2<T>(__uint_as_float(o[8 * q + 2]) * f, __uint_as_float(o[8 * q + 3]) * f);
-      v.z = pack2<T>(__uint_as_float(o[8 * q + 4]) * f, __uint_as_float(o[8 * q + 5]) * f);
-      v.w = pack2<T>(__uint_as_float(o[8 * q + 6]) * f, __uint_as_float(o[8 * q + 7]) * f);
-      out[q] = v;
+    for (int q = 0; q < N; ++q) {
+      v[q].x = pack2<T>(__uint_as_float(o[8 * q + 0]) * f, __uint_as_float(o[8 * q + 1]) * f);
+      v[q].y = pack2<T>(__uint_as_float(o[8 * q + 2]) * f, __uint_as_float(o[8 * q + 3]) * f);
+      v[q].z = pack2<T>(__uint_as_float(o[8 * q + 4]) * f, __uint_as_float(o[8 * q + 5]) * f);
+      v[q].w = pack2<T>(__uint_as_float(o[8 * q + 6]) * f, __uint_as_float(o[8 * q + 7]) * f);
     }
+  }
+#pragma unroll
+  for (int b = 1; b < N; b *= 2) {
+    const bool up = lane & b;
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+      if (q & b) continue;
+      uint4 &lo = v[q], &hi = v[q | b];
+      uint4 t = up ? lo : hi;
+      t.x = __shfl_xor_sync(0xffffffffu, t.x, b);
+      t.y = __shfl_xor_sync(0xffffffffu, t.y, b);
+      t.z = __shfl_xor_sync(0xffffffffu, t.z, b);
+      t.w = __shfl_xor_sync(0xffffffffu, t.w, b);
+      if (up) lo = t;
+      else hi = t;
+    }
+  }
+  // v[q] is now piece c of the row of lane (lane - c + q)
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    T* dst = reinterpret_cast<T*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), lane - c + q));
+    if (dst) *reinterpret_cast<uint4*>(dst + c * 8) = v[q];
   }
 }
 
@@ -366,11 +390,11 @@ __device__ void dq_elementwise(const CrossParams& p, float* red, uint32_t tbase,
   };
   float lse = row_constant(blockIdx.x);
   T* pend = nullptr;                   // dq row of the item whose accumulator is still to be read
-  bool pending = false, pend_on = false;
+  bool pending = false;
   auto finish = [&]() {
     if (!wait.warp(C::B_AF, (items - 1) & 1)) return false;
     tc_fence_after();
-    store_half<T, D>(tAcc, pend, p.scale, pend_on);
+    store_half<T, D>(tAcc, pend, p.scale);
     tc_fence_before();
     warp_arrive(bar + 8 * C::B_AE);
     pending = false;
@@ -461,8 +485,7 @@ __device__ void dq_elementwise(const CrossParams& p, float* red, uint32_t tbase,
     }
     ++items;
     pending = true;
-    pend = out;
-    pend_on = real;
+    pend = real ? out : nullptr;
   }
   if (pending) finish();
 }
@@ -619,34 +642,46 @@ __device__ void dkv_producer(const CrossMaps& m, const CrossParams& p, uint32_t 
   }
 }
 
+// The rows' constants, four rows a lane, fetched two steps before they are stored: a step is shorter
+// than a fetch from memory.
 template <int D>
 __device__ void dkv_rows(const CrossParams& p, float* aux, const Waiter& wait) {
   using C = CfgK<D>;
+  struct Rows {
+    float nl[4], nd[4];
+  };
   const int lane = threadIdx.x & 31;
+  auto fetch = [&](const ItemK& w, int i) {
+    Rows v;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = lane + 32 * k, tr = r / p.group, tok = i * p.toks + tr, h = w.hk * p.group + r - tr * p.group;
+      v.nl[k] = neg_inf();
+      v.nd[k] = 0.f;
+      if (i < w.q1 && tr < p.toks && tok < p.nq) {
+        const int64_t row = ((int64_t)w.b * p.heads + h) * p.nq + tok;
+        v.nl[k] = __ldg(p.lse + row);
+        v.nd[k] = __ldg(p.delta + row);
+      }
+    }
+    return v;
+  };
   Ring<C::NA> ra;
   for (int it = blockIdx.x; it < p.total; it += gridDim.x) {
     const ItemK w(p, it);
+    Rows a = fetch(w, w.q0), b = fetch(w, w.q0 + 1);
     for (int i = w.q0; i < w.q1; ++i, ++ra.n) {
-      float nl[4], nd[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int r = lane + 32 * k, tr = r / p.group, tok = i * p.toks + tr, h = w.hk * p.group + r - tr * p.group;
-        nl[k] = neg_inf();
-        nd[k] = 0.f;
-        if (tr < p.toks && tok < p.nq) {
-          const int64_t row = ((int64_t)w.b * p.heads + h) * p.nq + tok;
-          nl[k] = neg_lse2(__ldg(p.lse + row));
-          nd[k] = -__ldg(p.delta + row);
-        }
-      }
+      const Rows c = fetch(w, i + 2);
       if (!wait.warp(C::B_XE + ra.slot(), ra.phase() ^ 1)) return;
-      float* a = aux + ra.slot() * 256;
+      float* x = aux + ra.slot() * 256;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        a[lane + 32 * k] = nl[k];
-        a[128 + lane + 32 * k] = nd[k];
+        x[lane + 32 * k] = neg_lse2(a.nl[k]);
+        x[128 + lane + 32 * k] = -a.nd[k];
       }
       warp_arrive(wait.bar + 8 * (C::B_XF + ra.slot()));
+      a = b;
+      b = c;
     }
   }
 }
@@ -746,8 +781,8 @@ __device__ void dkv_elementwise(const CrossParams& p, const float* aux, uint32_t
           for (int q = 0; q < 8; ++q) dst[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
         }
     } else {
-      store_half<T, D>(tAcc, pend_v, 1.0f, pend_vis);
-      store_half<T, D>(tAcc + D, pend_k, p.scale, pend_vis);
+      store_half<T, D>(tAcc, pend_vis ? pend_v : nullptr, 1.0f);
+      store_half<T, D>(tAcc + D, pend_vis ? pend_k : nullptr, p.scale);
     }
     tc_fence_before();
     warp_arrive(bar + 8 * C::B_AE);
