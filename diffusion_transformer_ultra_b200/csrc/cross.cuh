@@ -41,6 +41,9 @@ __device__ __forceinline__ int cross_len(const CrossParams& p, int b) {
   return p.lens ? cross_clamp_len(__ldg(p.lens + b), p.ns) : p.ns;
 }
 
+// Query of a row of a packed query tile (r < 128), relative to the tile's first.
+__device__ __forceinline__ int row_tok(const CrossParams& p, int r) { return (r * p.group_inv) >> 16; }
+
 // Visibility of the 128 keys of tile j of sample b: bit c % 32 of word c / 32.
 __device__ __forceinline__ uint4 cross_words(const CrossParams& p, int b, int j, int len) {
   if (p.words) return __ldg(reinterpret_cast<const uint4*>(p.words) + (int64_t)b * p.word_tiles + j);

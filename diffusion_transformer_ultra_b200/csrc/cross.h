@@ -7,6 +7,8 @@
 
 #include <cstdint>
 
+#include "kernels.h"
+
 namespace ug {
 
 // Query rows are packed by key/value head: row tok * group + g of a unit (sample b, key/value
@@ -15,9 +17,11 @@ namespace ug {
 // behind them (group not a divisor of 128) stay zero.
 struct CrossParams {
   int batch, nq, ns, heads, kv_heads, group, toks;
+  int group_inv;                   // ceil(2^16 / group): r / group = (r * group_inv) >> 16 for r < 128
   int units, nqt;                  // batch * kv_heads; query tiles per unit
   int total;                       // work items of the launch
   int per_item;                    // query tiles of an item (1 or 2)
+  FastDiv div_h, div_kv, div_q, div_kt, div_split;   // by heads, kv_heads, items along the queries, key tiles, nsplit
   int nitem_q;                     // items along a unit's queries: ceil(nqt / per_item)
   int nsplit;                      // items along its keys (backward: along its queries)
   float scale, scale_log2;         // scale, scale * log2(e)
@@ -29,18 +33,18 @@ struct CrossParams {
   // tensors written or read by threads: base and batch, row, head strides (elements)
   void* out[3];                    // forward: o; dQ kernel: dq; dK/dV kernel: dk, dv
   int64_t out_st[3][3];
-  const void* o;                   // dQ kernel: o and do of the rows, for delta
+  const void* o;                   // backward: o and do of the rows, for delta
   const void* d_o;
   int64_t o_st[3], do_st[3];
   float* lse;                      // [batch][heads][nq]; forward: output or null, backward: input
-  float* delta;                    // backward: [batch][heads][nq], written by the dQ kernel
+  float* delta;                    // backward: [batch][heads][nq] do . o
   float* part;                     // partial results of split items (null: nsplit == 1)
   int part_rows;                   // rows stored per (unit, query tile, split)
   unsigned long long timeout_ns;
 };
 
 struct CrossMaps {
-  CUtensorMap q, k, v, d_o, o;
+  CUtensorMap q, k, v, d_o;
 };
 
 // Keys [0, len) of sample b may be visible.

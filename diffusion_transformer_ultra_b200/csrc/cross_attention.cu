@@ -106,6 +106,7 @@ void schedule(const ultragen_cross_t* c, int sms, CrossParams& p) {
   p.units = c->batch * c->kv_heads;
   p.group = c->heads / c->kv_heads;
   p.toks = 128 / p.group;
+  p.group_inv = (65536 + p.group - 1) / p.group;
   p.nqt = (c->nq + p.toks - 1) / p.toks;
   const int kt = std::max(1, (c->ns + 127) / 128);
   p.per_item = (int64_t)p.units * ((p.nqt + 1) / 2) >= sms && p.nqt > 1 ? 2 : 1;
@@ -121,6 +122,8 @@ void schedule(const ultragen_cross_t* c, int sms, CrossParams& p) {
     }
   }
   p.total = (int)(items * p.nsplit);
+  p.div_q = FastDiv((uint32_t)std::max(1, p.nitem_q));
+  p.div_split = FastDiv((uint32_t)p.nsplit);
   p.part_rows = p.nqt == 1 ? p.group * c->nq : 128;
 }
 
@@ -150,6 +153,7 @@ Layout backward_layout(const ultragen_cross_t* c, CrossParams& p) {
   p.units = c->batch * c->kv_heads;
   p.group = c->heads / c->kv_heads;
   p.toks = 128 / p.group;
+  p.group_inv = (65536 + p.group - 1) / p.group;
   p.nqt = (c->nq + p.toks - 1) / p.toks;
   const int64_t tiles = (int64_t)p.units * ((c->ns + 127) / 128);
   int64_t best = 0;
@@ -162,6 +166,9 @@ Layout backward_layout(const ultragen_cross_t* c, CrossParams& p) {
     }
   }
   p.total = (int)(tiles * p.nsplit);
+  p.div_q = FastDiv((uint32_t)std::max(1, p.nqt));
+  p.div_kt = FastDiv((uint32_t)std::max(1, (c->ns + 127) / 128));
+  p.div_split = FastDiv((uint32_t)std::max(1, p.nsplit));
   Layout l = mask_layout(c);
   l.delta = pad16((size_t)c->batch * c->heads * c->nq * 4);
   if (p.nsplit > 1) l.part = (size_t)p.total * 2 * 128 * c->head_dim * 4;
@@ -201,6 +208,8 @@ void common(const ultragen_cross_t* c, const int32_t* lens, const uint8_t* mask,
   p.ns = c->ns;
   p.heads = c->heads;
   p.kv_heads = c->kv_heads;
+  p.div_h = FastDiv((uint32_t)c->heads);
+  p.div_kv = FastDiv((uint32_t)c->kv_heads);
   p.scale = c->scale;
   p.scale_log2 = (float)(c->scale * 1.4426950408889634);
   p.lens = lens;
@@ -336,8 +345,7 @@ int ultragen_cross_attention_backward(const ultragen_cross_t* c, const void* d_o
   std::memset(&m, 0, sizeof(m));
   if (c->nq > 0 &&
       ((st = make_map(&m.q, q, sd[0], c->dtype, c->batch, c->nq, c->kv_heads, p.group, c->head_dim, p.toks)) ||
-       (st = make_map(&m.d_o, d_o, sd[4], c->dtype, c->batch, c->nq, c->kv_heads, p.group, c->head_dim, p.toks)) ||
-       (st = make_map(&m.o, o, sd[3], c->dtype, c->batch, c->nq, c->kv_heads, p.group, c->head_dim, p.toks))))
+       (st = make_map(&m.d_o, d_o, sd[4], c->dtype, c->batch, c->nq, c->kv_heads, p.group, c->head_dim, p.toks))))
     return st;
   if (c->ns > 0 &&
       ((st = make_map(&m.k, k, sd[1], c->dtype, c->batch, c->ns, c->kv_heads, 1, c->head_dim, 128)) ||

@@ -14,6 +14,7 @@
 // TMEM lane quarter w % 4 and half the columns), warp 8 producer (TMA), warp 9 MMA issuer.
 // Steps of consecutive items run on without a drain: the products of a step are issued around
 // the one before it, so that the tensor core works while the elementwise part of a step runs.
+#include <algorithm>
 #include <cstdint>
 #include <mutex>
 
@@ -38,11 +39,11 @@ struct Ring {
 
 struct Waiter {
   uint32_t bar;                        // first barrier
-  volatile int* abort_flag;
+  uint32_t abort_word;
   int code;
-  uint64_t timeout_ns;
+  uint32_t limit_ns;
   __device__ __forceinline__ bool operator()(int b, uint32_t parity) const {
-    return mbar_wait(bar + 8 * b, parity, abort_flag, &g_error, code, timeout_ns);
+    return mbar_wait_short(bar + 8 * b, parity, abort_word, code, limit_ns);
   }
   // all lanes of the warp
   __device__ __forceinline__ bool warp(int b, uint32_t parity) const {
@@ -53,11 +54,17 @@ struct Waiter {
   }
 };
 
-// Waits (bounded) for the copies in flight of a ring of N slots at barrier b: none may land after
+// At a kernel's end: a wait that ran out.
+__device__ __forceinline__ void report(const uint32_t* abort_word) {
+  const int code = *reinterpret_cast<const volatile int*>(abort_word);
+  if (threadIdx.x == 0 && code != 0) atomicExch(&g_error, code);
+}
+
+// After a wait that ran out: the copies in flight land well within this time, and none may land after
 // this CTA exits.
-template <int N>
-__device__ __forceinline__ void drain_ring(const Waiter& wait, int b, const Ring<N>& r) {
-  for (uint32_t i = r.n >= N ? r.n - N : 0; i < r.n; ++i) wait.drain(b + i % N, (i / N) & 1);
+__device__ __noinline__ void settle() {
+  const uint64_t t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < kDrainNs) __nanosleep(1000);
 }
 
 __device__ __forceinline__ void warp_arrive(uint32_t bar) {
@@ -69,44 +76,34 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
 template <int D>
 __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* m, int row, int hk, int b, uint32_t bar) {
 #pragma unroll
-  for (int bx = 0; bx < D / 64; ++bx) tma_load_5d(dst + bx * BOX_BYTES, m, bx * 64, 0, row, hk, b, bar);
+  for (int bx = 0; bx < D / 64; ++bx) tma_load_5d_elect(dst + bx * BOX_BYTES, m, bx * 64, 0, row, hk, b, bar);
 }
 
 // D[128 x 128] = A B^T over K = D, both tiles K-major.
 template <typename T, int D>
 __device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b) {
-  const uint32_t alo = desc_lo(a, 16), blo = desc_lo(b, 16);
-#pragma unroll
-  for (int kk = 0; kk < D / 16; ++kk) {
-    const uint32_t off = ((kk / 4) * BOX_BYTES + (kk % 4) * 32) >> 4;
-    mma_ss_elect(d, alo + off, blo + off, desc_hi_sw128(1024), idesc_half<T>(128, 128, 0), kk > 0 ? 1u : 0u);
-  }
+  mma_ss_tile_elect<D>(d, desc_lo(a, 16), desc_lo(b, 16), desc_hi_sw128(1024), idesc_half<T>(128, 128, 0));
 }
 
-// D[128 x D] (+)= A B: A is a packed 16-bit operand in TMEM, its columns 64 h .. 64 h + 63 at
-// column a + 64 h (32 columns); B a [128 x D] tile read MN-major.
+// D[128 x D] (+)= A B: A a packed 16-bit operand in TMEM, B a [128 x D] tile read MN-major.
 template <typename T, int D>
 __device__ __forceinline__ void mma_accum(uint32_t d, uint32_t a, uint32_t b, bool first) {
-  const uint32_t blo = desc_lo(b, BOX_BYTES);
-#pragma unroll
-  for (int kk = 0; kk < 8; ++kk)
-    mma_ts_elect(d, a + (kk / 4) * 64 + (kk % 4) * 8, blo + kk * (2048 >> 4), desc_hi_sw128(1024), idesc_half<T>(128, D, 1),
-             (first && kk == 0) ? 0u : 1u);
+  mma_ts_tile_elect(d, a, desc_lo(b, BOX_BYTES), desc_hi_sw128(1024), idesc_half<T>(128, D, 1), first ? 0u : 1u);
 }
 
-// Half a row of an accumulator per lane, scaled and rounded, to 16-bit global memory.  Stores by row
-// would go to 32 rows each; N = D / 16 lanes exchange their 16-byte pieces first (a transpose of N x N
-// pieces in log2(N) rounds), so that N lanes write one row's piece of 32 N / 2 bytes together.  `row`
-// is the lane's destination, null for a row that is not stored.
-template <typename T, int D>
-__device__ __forceinline__ void store_half(uint32_t tmem, T* row, float f) {
-  constexpr int N = D / 16;
+// W columns of a row of an accumulator per lane, scaled and rounded, to 16-bit global memory.  Stores
+// by row would go to 32 rows each; N = W / 8 lanes exchange their 16-byte pieces first (a transpose of
+// N x N pieces in log2(N) rounds), so that N lanes write one row's 2 W bytes together.  `row` is the
+// lane's destination, null for a row that is not stored.
+template <typename T, int W>
+__device__ __forceinline__ void store_piece(uint32_t tmem, T* row, float f) {
+  constexpr int N = W / 8;
   const int lane = threadIdx.x & 31, c = lane & (N - 1);
   uint4 v[N];
   {
-    uint32_t o[D / 2];
+    uint32_t o[W];
     __syncwarp();
-    if constexpr (D == 128) tmem_ld64_sync(tmem, o);
+    if constexpr (W == 64) tmem_ld64_sync(tmem, o);
     else tmem_ld32_sync(tmem, o);
 #pragma unroll
     for (int q = 0; q < N; ++q) {
@@ -146,13 +143,35 @@ __device__ __forceinline__ void zero_half(T* dst) {
   for (int q = 0; q < D / 16; ++q) reinterpret_cast<uint4*>(dst)[q] = make_uint4(0, 0, 0, 0);
 }
 
+// Visibility of 32 columns as masks of packed pairs: bit 2 c goes to bit c, bit 2 c + 1 to bit 16 + c;
+// a pair's mask is then a shift and a byte permutation that repeats the signs of two bytes.
+__device__ __forceinline__ uint32_t split_pairs(uint32_t w) {
+  uint32_t t;
+  t = (w ^ (w >> 1)) & 0x22222222u;
+  w ^= t ^ (t << 1);
+  t = (w ^ (w >> 2)) & 0x0c0c0c0cu;
+  w ^= t ^ (t << 2);
+  t = (w ^ (w >> 4)) & 0x00f000f0u;
+  w ^= t ^ (t << 4);
+  t = (w ^ (w >> 8)) & 0x0000ff00u;
+  return w ^ t ^ (t << 8);
+}
+__device__ __forceinline__ uint32_t pair_mask(uint32_t w, int c) {
+  uint32_t m;
+  asm("prmt.b32 %0, %1, 0, 0xbb99;" : "=r"(m) : "r"(w << (15 - c)));
+  return m;
+}
+
 // -lse log2(e), the constant of a row's exponentials; -inf (P = 0) for a row that does not exist
 // or has no visible key.
 __device__ __forceinline__ float neg_lse2(float lse) { return lse == neg_inf() ? neg_inf() : -lse * 1.4426950408889634f; }
 
 // ---------------------------------------------------------------------------------- dQ
-// 512 threads: warps 10 (scrubber: zeroes hidden K rows, which may hold NaN: 0 * NaN), 12-15
-// (delta = do . o of the next items' rows, from global memory, two items ahead).
+// 512 threads: warps 10 (scrubber: zeroes hidden K rows, which may hold NaN: 0 * NaN), 12-15 (the
+// accumulators' way to dq: the elementwise warps are what a step waits for).  delta = do . o comes from
+// a kernel before: made by warps 12-15 in here, its code and the other roles' did not fit the
+// instruction cache together (156 misses a step), and the pass took 218 us instead of 25 + 1XX at
+// 4 x 4,096 queries x 512 keys x 24 heads of 128.
 // TMEM: S [0,128), dP / dS in two buffers [128,384), dQ [384,384+D).
 template <int D>
 struct CfgQ {
@@ -162,17 +181,16 @@ struct CfgQ {
   static constexpr int RED_OFF = V_OFF + NV * TILE;            // [2][2][128] floats: halves of a row's sum
   static constexpr int BAR_OFF = RED_OFF + 4 * 128 * 4;
   // full / empty of Q, dO, K (full, scrubbed, empty), V; S ready / read; dP ready; dS ready;
-  // accumulator ready / read; delta ready / read; halves exchanged
+  // accumulator ready / read; halves exchanged
   static constexpr int B_QF = 0, B_QE = 1, B_OF = 2, B_OE = 3, B_KF = 4, B_KS = B_KF + NK, B_KE = B_KS + NK, B_VF = B_KE + NK,
                        B_VE = B_VF + NV, B_SF = B_VE + NV, B_SR = B_SF + 1, B_PF = B_SR + 1, B_DS = B_PF + 2, B_AF = B_DS + 1,
-                       B_AE = B_AF + 1, B_DF = B_AE + 1, B_DE = B_DF + 2, B_XR = B_DE + 2, B_DRAIN = B_XR + 1,
+                       B_AE = B_AF + 1, B_XR = B_AE + 1, B_DRAIN = B_XR + 1,
                        NBAR = B_DRAIN + 1;
   static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
   static constexpr int SMEM = MISC_OFF + 16;
   static_assert(SMEM <= 227 * 1024, "shared memory per CTA exceeds 227 KB");
   static __device__ __forceinline__ uint32_t arrivals(int i) {
-    if (i == B_SR || i == B_DS || i == B_AE || i == B_XR || i == B_DE || i == B_DE + 1) return 8;   // elementwise warps
-    return i == B_DF || i == B_DF + 1 ? 4 : 1;                                                       // delta warps
+    return i == B_SR || i == B_DS || i == B_XR ? 8 : (i == B_AE ? 4 : 1);   // elementwise warps; warps 12-15
   }
 };
 constexpr int kThreadsQ = 512, kRegsLaunchQ = 128, kRegsElemQ = 184, kRegsOtherQ = 72;
@@ -181,9 +199,9 @@ static_assert(256 * kRegsElemQ + 256 * kRegsOtherQ <= kThreadsQ * kRegsLaunchQ, 
 struct ItemQ {
   int b, hk, qt, len, n;
   __device__ __forceinline__ ItemQ(const CrossParams& p, int it) {
-    const uint32_t u = (uint32_t)it / p.nqt;
+    const uint32_t u = p.div_q.div(it);
     qt = it - u * p.nqt;
-    b = u / p.kv_heads;
+    b = p.div_kv.div(u);
     hk = u - b * p.kv_heads;
     len = cross_len(p, b);
     n = (len + 127) >> 7;
@@ -201,47 +219,41 @@ __device__ void dq_producer(const CrossMaps& m, const CrossParams& p, uint32_t s
   bool ok = true;
   for (int it = blockIdx.x; ok && it < p.total; it += gridDim.x) {
     const ItemQ w(p, it);
-    const int ahead = it + 2 * (int)gridDim.x;
-    if (ahead < p.total) {             // (total + 2 grids stays below 2^31: see the entry point's check)
-      // the rows of the item after next into L2: delta reads them an item ahead of the products
-      const ItemQ a(p, ahead);
+    const int n = uniform(w.n);
+    const int ahead = it + (int)gridDim.x;
+    if (ahead < p.total) {             // (total + a grid stays below 2^31: see the entry point's check)
+      const ItemQ a(p, ahead);         // the next item's rows into L2: their slots free late
 #pragma unroll
       for (int bx = 0; bx < D / 64; ++bx) {
-        tma_prefetch_5d(&m.o, bx * 64, 0, a.qt * p.toks, a.hk, a.b);
-        tma_prefetch_5d(&m.d_o, bx * 64, 0, a.qt * p.toks, a.hk, a.b);
-        tma_prefetch_5d(&m.q, bx * 64, 0, a.qt * p.toks, a.hk, a.b);
+        tma_prefetch_5d_elect(&m.q, bx * 64, 0, a.qt * p.toks, a.hk, a.b);
+        tma_prefetch_5d_elect(&m.d_o, bx * 64, 0, a.qt * p.toks, a.hk, a.b);
       }
     }
-    for (int j = 0; j < w.n; ++j) {
+    for (int j = 0; j < n; ++j) {
       if (j == 0) {
-        if (!(ok = wait(C::B_QE, rq.phase() ^ 1))) break;
-        mbar_expect_tx(bar + 8 * C::B_QF, q_bytes);
+        if (!(ok = wait.warp(C::B_QE, rq.phase() ^ 1))) break;
+        mbar_expect_tx_elect(bar + 8 * C::B_QF, q_bytes);
         load_tile<D>(sbase, &m.q, w.qt * p.toks, w.hk, w.b, bar + 8 * C::B_QF);
         ++rq.n;
       }
       const uint32_t ks = rk.slot(), vs = rv.slot();
-      if (!(ok = wait(C::B_KE + ks, rk.phase() ^ 1))) break;
-      mbar_expect_tx(bar + 8 * (C::B_KF + ks), C::TILE);
+      if (!(ok = wait.warp(C::B_KE + ks, rk.phase() ^ 1))) break;
+      mbar_expect_tx_elect(bar + 8 * (C::B_KF + ks), C::TILE);
       load_tile<D>(sbase + C::K_OFF + ks * C::TILE, &m.k, j * 128, w.hk, w.b, bar + 8 * (C::B_KF + ks));
       ++rk.n;
       if (j == 0) {
-        if (!(ok = wait(C::B_OE, ro.phase() ^ 1))) break;
-        mbar_expect_tx(bar + 8 * C::B_OF, q_bytes);
+        if (!(ok = wait.warp(C::B_OE, ro.phase() ^ 1))) break;
+        mbar_expect_tx_elect(bar + 8 * C::B_OF, q_bytes);
         load_tile<D>(sbase + C::DO_OFF, &m.d_o, w.qt * p.toks, w.hk, w.b, bar + 8 * C::B_OF);
         ++ro.n;
       }
-      if (!(ok = wait(C::B_VE + vs, rv.phase() ^ 1))) break;
-      mbar_expect_tx(bar + 8 * (C::B_VF + vs), C::TILE);
+      if (!(ok = wait.warp(C::B_VE + vs, rv.phase() ^ 1))) break;
+      mbar_expect_tx_elect(bar + 8 * (C::B_VF + vs), C::TILE);
       load_tile<D>(sbase + C::V_OFF + vs * C::TILE, &m.v, j * 128, w.hk, w.b, bar + 8 * (C::B_VF + vs));
       ++rv.n;
     }
   }
-  if (!ok) {
-    drain_ring(wait, C::B_QF, rq);
-    drain_ring(wait, C::B_OF, ro);
-    drain_ring(wait, C::B_KF, rk);
-    drain_ring(wait, C::B_VF, rv);
-  }
+  if (!ok) settle();
 }
 
 template <int D>
@@ -262,49 +274,33 @@ __device__ void dq_scrub(const CrossParams& p, uint32_t sbase, const Waiter& wai
   }
 }
 
-// delta of the rows of items with more than one key tile (see dq_elementwise), to global memory.
-// Four warps, 32 rows each; D / 8 lanes per row.
+// The accumulators' way to dq (zeros where no key is visible).  Four warps, 32 rows each.
 template <typename T, int D>
-__device__ void dq_delta(const CrossParams& p, const Waiter& wait) {
+__device__ void dq_store(const CrossParams& p, uint32_t tbase, const Waiter& wait) {
   using C = CfgQ<D>;
-  constexpr int LPR = D / 8, RPW = 32 / LPR;            // lanes per row, rows per load
-  const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
-  Ring<2> rd;
+  const int r = threadIdx.x & 127, tr = row_tok(p, r), gr = r - tr * p.group;
+  const uint32_t tAcc = tbase + ((uint32_t)((threadIdx.x >> 5) & 3) * 32u << 16) + 384;
+  uint32_t items = 0;
   for (int it = blockIdx.x; it < p.total; it += gridDim.x) {
     const ItemQ w(p, it);
-    if (w.n < 2) continue;
-    if (!wait.warp(C::B_DE + rd.slot(), rd.phase() ^ 1)) return;
-#pragma unroll 1
-    for (int r0 = 0; r0 < 32; r0 += 4 * RPW) {
-      uint4 a[4] = {}, g[4] = {};
-      int64_t row[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = warp * 32 + r0 + i * RPW + lane / LPR;
-        const int tr = r / p.group, tok = w.qt * p.toks + tr, h = w.hk * p.group + r - tr * p.group;
-        row[i] = -1;
-        if (tr < p.toks && tok < p.nq) {
-          row[i] = ((int64_t)w.b * p.heads + h) * p.nq + tok;
-          const int c = lane % LPR * 8;
-          a[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.o) + w.b * p.o_st[0] + tok * p.o_st[1] + h * p.o_st[2] + c));
-          g[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.d_o) + w.b * p.do_st[0] + tok * p.do_st[1] +
-                                                      h * p.do_st[2] + c));
-        }
+    const int tok = w.qt * p.toks + tr;
+    T* out = nullptr;
+    if (tr < p.toks && tok < p.nq)
+      out = static_cast<T*>(p.out[0]) + w.b * p.out_st[0][0] + tok * p.out_st[0][1] + (w.hk * p.group + gr) * p.out_st[0][2];
+    if (w.n == 0) {
+      if (out) {
+        zero_half<T, D>(out);
+        zero_half<T, D>(out + D / 2);
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const T* av = reinterpret_cast<const T*>(&a[i]);
-        const T* gv = reinterpret_cast<const T*>(&g[i]);
-        float s = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s += to_f32(av[e]) * to_f32(gv[e]);
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (lane % LPR == 0 && row[i] >= 0) p.delta[row[i]] = s;
-      }
+      continue;
     }
-    warp_arrive(wait.bar + 8 * (C::B_DF + rd.slot()));
-    ++rd.n;
+    if (!wait.warp(C::B_AF, items & 1)) return;
+    tc_fence_after();
+#pragma unroll 1
+    for (int ch = 0; ch < D / 32; ++ch) store_piece<T, 32>(tAcc + ch * 32, out ? out + ch * 32 : nullptr, p.scale);
+    tc_fence_before();
+    warp_arrive(wait.bar + 8 * C::B_AE);
+    ++items;
   }
 }
 
@@ -319,35 +315,38 @@ __device__ void dq_mma(const CrossParams& p, uint32_t sbase, uint32_t tbase, con
   uint32_t g = 0, items = 0;           // steps and items begun
   bool ok = true, pending = false, pfirst = false, plast = false;
   uint32_t pslot = 0, pitem = 0;
-  // dQ += dS K of step g - 1
-  auto accumulate = [&]() {
-    if (!wait.warp(C::B_DS, (g - 1) & 1)) return false;
-    if (pfirst && pitem > 0 && !wait.warp(C::B_AE, (pitem - 1) & 1)) return false;
-    tc_fence_after();
-    mma_accum<T, D>(tAcc, tbase + 128 + 128 * ((g - 1) & 1), sbase + C::K_OFF + pslot * C::TILE, pfirst);
-    mma_commit_elect(bar + 8 * (C::B_KE + pslot));
-    if (plast) mma_commit_elect(bar + 8 * C::B_AF);
-    return true;
-  };
-  for (int it = blockIdx.x; ok && it < p.total; it += gridDim.x) {
-    const int n = uniform(ItemQ(p, it).n);
+  // one round more than there are items: the last step's product (each product has one place in
+  // the code, which the warps of all roles share the instruction cache with)
+  for (int it = blockIdx.x; ok; it += gridDim.x) {
+    const bool end = it >= p.total;
+    const int n = end ? 1 : uniform(ItemQ(p, it).n);
     for (int j = 0; j < n; ++j) {
-      if (j == 0 && !(ok = wait.warp(C::B_QF, rq.phase()))) break;
-      if (!(ok = wait.warp(kready + rk.slot(), rk.phase()))) break;
-      if (g > 0 && !(ok = wait.warp(C::B_SR, (g - 1) & 1))) break;
-      tc_fence_after();
-      mma_scores<T, D>(tbase, sbase, sbase + C::K_OFF + rk.slot() * C::TILE);
-      mma_commit_elect(bar + 8 * C::B_SF);
-      if (j == n - 1) mma_commit_elect(bar + 8 * C::B_QE);
-      if (j == 0 && !(ok = wait.warp(C::B_OF, rq.phase()))) break;
-      if (!(ok = wait.warp(C::B_VF + rv.slot(), rv.phase()))) break;
-      tc_fence_after();
-      // (overwrites dS of step g - 2, which the product issued before has read)
-      mma_scores<T, D>(tbase + 128 + 128 * (g & 1), sbase + C::DO_OFF, sbase + C::V_OFF + rv.slot() * C::TILE);
-      mma_commit_elect(bar + 8 * (C::B_PF + (g & 1)));
-      mma_commit_elect(bar + 8 * (C::B_VE + rv.slot()));
-      if (j == n - 1) mma_commit_elect(bar + 8 * C::B_OE);
-      if (pending && !(ok = accumulate())) break;
+      if (!end) {
+        if (j == 0 && !(ok = wait.warp(C::B_QF, rq.phase()))) break;
+        if (!(ok = wait.warp(kready + rk.slot(), rk.phase()))) break;
+        if (g > 0 && !(ok = wait.warp(C::B_SR, (g - 1) & 1))) break;
+        tc_fence_after();
+        mma_scores<T, D>(tbase, sbase, sbase + C::K_OFF + rk.slot() * C::TILE);
+        mma_commit_elect(bar + 8 * C::B_SF);
+        if (j == n - 1) mma_commit_elect(bar + 8 * C::B_QE);
+        if (j == 0 && !(ok = wait.warp(C::B_OF, rq.phase()))) break;
+        if (!(ok = wait.warp(C::B_VF + rv.slot(), rv.phase()))) break;
+        tc_fence_after();
+        // (overwrites dS of step g - 2, which the product issued before has read)
+        mma_scores<T, D>(tbase + 128 + 128 * (g & 1), sbase + C::DO_OFF, sbase + C::V_OFF + rv.slot() * C::TILE);
+        mma_commit_elect(bar + 8 * (C::B_PF + (g & 1)));
+        mma_commit_elect(bar + 8 * (C::B_VE + rv.slot()));
+        if (j == n - 1) mma_commit_elect(bar + 8 * C::B_OE);
+      }
+      if (pending) {                   // dQ += dS K of step g - 1
+        if (!(ok = wait.warp(C::B_DS, (g - 1) & 1))) break;
+        if (pfirst && pitem > 0 && !(ok = wait.warp(C::B_AE, (pitem - 1) & 1))) break;
+        tc_fence_after();
+        mma_accum<T, D>(tAcc, tbase + 128 + 128 * ((g - 1) & 1), sbase + C::K_OFF + pslot * C::TILE, pfirst);
+        mma_commit_elect(bar + 8 * (C::B_KE + pslot));
+        if (plast) mma_commit_elect(bar + 8 * C::B_AF);
+      }
+      if (end) return;
       pending = true;
       pfirst = j == 0;
       plast = j == n - 1;
@@ -362,71 +361,51 @@ __device__ void dq_mma(const CrossParams& p, uint32_t sbase, uint32_t tbase, con
       ++items;
     }
   }
-  if (ok && pending) ok = accumulate();
-  if (!ok) {
-    mma_commit_elect(bar + 8 * C::B_DRAIN);
-    wait.drain(C::B_DRAIN, 0);
-  }
+  mma_commit_elect(bar + 8 * C::B_DRAIN);
+  wait.drain(C::B_DRAIN, 0);
 }
 
+// The elementwise part.  delta comes from do . o, except where all of a row's keys are in one tile:
+// there it is sum_j p_j dP_j, without the rounding of o, which matters where few keys share the weight.
 template <typename T, int D>
 __device__ void dq_elementwise(const CrossParams& p, float* red, uint32_t tbase, const Waiter& wait) {
   using C = CfgQ<D>;
   const uint32_t bar = wait.bar;
   const int half = threadIdx.x >> 7, r = threadIdx.x & 127;
   const uint32_t lane_off = (uint32_t)((threadIdx.x >> 5) & 3) * 32u << 16;
-  const uint32_t tS = tbase + lane_off + half * 64, tP = tS + 128, tAcc = tbase + lane_off + 384 + half * (D / 2);
-  const int tok_r = r / p.group, g_r = r - tok_r * p.group;
+  const uint32_t tS = tbase + lane_off + half * 64, tP = tS + 128;
+  const int tok_r = row_tok(p, r), g_r = r - tok_r * p.group;
   const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
-  uint32_t g = 0, items = 0, xn = 0;
-  Ring<2> rd;
-  // -lse log2(e) of this thread's row of item `it`, fetched an item ahead
-  auto row_constant = [&](int it) {
-    if (it >= p.total) return neg_inf();
-    const ItemQ w(p, it);
+  uint32_t g = 0, xn = 0;
+  // lse and delta of this thread's row of an item, fetched an item ahead
+  auto row_of = [&](const ItemQ& w) {
     const int tok = w.qt * p.toks + tok_r;
-    if (tok_r >= p.toks || tok >= p.nq) return neg_inf();
-    return __ldg(p.lse + ((int64_t)w.b * p.heads + w.hk * p.group + g_r) * p.nq + tok);
+    return tok_r < p.toks && tok < p.nq ? ((int64_t)w.b * p.heads + w.hk * p.group + g_r) * p.nq + tok : (int64_t)-1;
   };
-  float lse = row_constant(blockIdx.x);
-  T* pend = nullptr;                   // dq row of the item whose accumulator is still to be read
-  bool pending = false;
-  auto finish = [&]() {
-    if (!wait.warp(C::B_AF, (items - 1) & 1)) return false;
-    tc_fence_after();
-    store_half<T, D>(tAcc, pend, p.scale);
-    tc_fence_before();
-    warp_arrive(bar + 8 * C::B_AE);
-    pending = false;
-    return true;
+  float lse = neg_inf(), delta = 0.f;
+  auto fetch = [&](int it) {
+    lse = neg_inf();
+    if (it >= p.total) return;
+    const ItemQ w(p, it);
+    const int64_t row = row_of(w);
+    if (row < 0) return;
+    lse = __ldg(p.lse + row);
+    if (w.n > 1) delta = __ldg(p.delta + row);
   };
   for (int it = blockIdx.x; it < p.total; it += gridDim.x) {
+    if (it == blockIdx.x) fetch(it);
     const ItemQ w(p, it);
-    const int tok = w.qt * p.toks + tok_r, h = w.hk * p.group + g_r;
-    const bool real = tok_r < p.toks && tok < p.nq;
-    T* out = static_cast<T*>(p.out[0]) + w.b * p.out_st[0][0] + tok * p.out_st[0][1] + h * p.out_st[0][2] + half * (D / 2);
-    if (w.n == 0) {
-      if (real) zero_half<T, D>(out);
-      lse = row_constant(it + gridDim.x);
-      continue;
-    }
-    const int64_t row = ((int64_t)w.b * p.heads + h) * p.nq + tok;
     const float nl = neg_lse2(lse);
-    const float2 nl2 = make_float2(nl, nl);
-    lse = row_constant(it + gridDim.x);
+    float nd = -delta;                 // (not set with one key tile)
+    fetch(it + gridDim.x);
+    const int n = w.n;
+    if (n == 0) continue;
     // one visible key has weight one whatever its logit: dS is zero exactly
     const bool zero = w.len == 1 || (p.single && __ldg(p.single + w.b));
-    float nd = 0.f;                    // -delta
-    if (w.n > 1) {
-      if (!wait.warp(C::B_DF + rd.slot(), rd.phase())) return;
-      if (real) nd = -__ldcg(p.delta + row);
-      warp_arrive(bar + 8 * (C::B_DE + rd.slot()));
-      ++rd.n;
-    }
-    for (int j = 0; j < w.n; ++j) {
+    const float2 nl2 = make_float2(nl, nl);
+    for (int j = 0; j < n; ++j) {
       const uint4 vis = cross_words(p, w.b, j, w.len);
       const uint32_t w0 = half ? vis.z : vis.x, w1 = half ? vis.w : vis.y;
-      const bool part = (w0 & w1) != ~0u;
       uint32_t s[64];
       if (!wait.warp(C::B_SF, g & 1)) return;
       tc_fence_after();
@@ -443,14 +422,13 @@ __device__ void dq_elementwise(const CrossParams& p, float* red, uint32_t tbase,
       tc_fence_after();
       uint32_t d[64];
       tmem_ld64_sync(tP + 128 * (g & 1), d);
-      if (part) {                      // whatever hidden keys and values hold
+      const bool part = (w0 & w1) != ~0u;
+      if (n == 1) {
+        if (part) {                    // whatever hidden keys and values hold
 #pragma unroll
-        for (int c = 0; c < 64; ++c)
-          if (!(((c < 32 ? w0 : w1) >> (c & 31)) & 1u)) s[c] = d[c] = 0u;
-      }
-      if (w.n == 1) {
-        // all of a row's keys are here: delta = sum_j p_j dP_j, without the rounding of o, which
-        // matters where few keys share the weight
+          for (int c = 0; c < 64; ++c)
+            if (!(((c < 32 ? w0 : w1) >> (c & 31)) & 1u)) s[c] = d[c] = 0u;
+        }
         float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
         for (int c = 0; c < 32; ++c)
@@ -461,10 +439,10 @@ __device__ void dq_elementwise(const CrossParams& p, float* red, uint32_t tbase,
         x[half * 128 + r] = sum.x + sum.y;
         warp_arrive(bar + 8 * C::B_XR);
         if (!wait.warp(C::B_XR, xn & 1)) return;
-        const float delta = x[r] + x[128 + r];
+        nd = -(x[r] + x[128 + r]);
         ++xn;
-        nd = -delta;
-        if (real && half == 0) p.delta[row] = delta;
+        const int64_t row = row_of(w);
+        if (half == 0 && row >= 0) p.delta[row] = -nd;
       }
       const float2 nd2 = make_float2(nd, nd);
       uint32_t pk[32];
@@ -472,7 +450,12 @@ __device__ void dq_elementwise(const CrossParams& p, float* red, uint32_t tbase,
       for (int c = 0; c < 32; ++c) {
         const float2 x = fmul2(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])),
                                fadd2(make_float2(__uint_as_float(d[2 * c]), __uint_as_float(d[2 * c + 1])), nd2));
-        pk[c] = zero ? 0u : pack2<T>(x.x, x.y);
+        pk[c] = pack2<T>(x.x, x.y);
+      }
+      if (part || zero) {
+        const uint32_t m0 = zero ? 0u : split_pairs(w0), m1 = zero ? 0u : split_pairs(w1);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) pk[c] &= pair_mask(c < 16 ? m0 : m1, c & 15);
       }
       __syncwarp();
       tmem_st32(tP + 128 * (g & 1), pk);
@@ -480,14 +463,8 @@ __device__ void dq_elementwise(const CrossParams& p, float* red, uint32_t tbase,
       tc_fence_before();
       warp_arrive(bar + 8 * C::B_DS);
       ++g;
-      // the item before: its last product runs while this item's first step is worked on
-      if (pending && !finish()) return;
     }
-    ++items;
-    pending = true;
-    pend = real ? out : nullptr;
   }
-  if (pending) finish();
 }
 
 template <typename T, int D>
@@ -500,12 +477,11 @@ __global__ void __launch_bounds__(kThreadsQ, 1) cross_dq_kernel(const __grid_con
     return;
   }
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
   const uint32_t bar = sbase + C::BAR_OFF;
-  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5);
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NBAR; ++i) mbar_init(bar + 8 * i, C::arrivals(i));
-    *abort_flag = 0;
+    misc[1] = 0;                       // abort word
     fence_mbar_init();
   }
   if (p.toks * p.group < 128) {        // rows that no copy fills are read by the products
@@ -521,19 +497,19 @@ __global__ void __launch_bounds__(kThreadsQ, 1) cross_dq_kernel(const __grid_con
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = misc[0];
-  Waiter wait{bar, abort_flag, DEV_TIMEOUT_SOFTMAX, p.timeout_ns};
+  Waiter wait{bar, smem_u32(misc + 1), DEV_TIMEOUT_SOFTMAX, (uint32_t)p.timeout_ns};
   if (warp >= 8) {
     regs_shrink<kRegsOtherQ>();
     if (warp == kWarpProducer) {
       wait.code = DEV_TIMEOUT_PRODUCER;
-      if (lane == 0) dq_producer<D>(m, p, sbase, wait);
+      dq_producer<D>(m, p, sbase, wait);
     } else if (warp == kWarpMma) {
       wait.code = DEV_TIMEOUT_MMA;
       dq_mma<T, D>(p, sbase, uniform(tbase), wait);
     } else if (warp == kWarpAux) {
       if (p.scrub) dq_scrub<D>(p, sbase, wait);
     } else if (warp >= 12) {
-      dq_delta<T, D>(p, wait);
+      dq_store<T, D>(p, tbase, wait);
     }
   } else {
     regs_grow<kRegsElemQ>();
@@ -542,9 +518,47 @@ __global__ void __launch_bounds__(kThreadsQ, 1) cross_dq_kernel(const __grid_con
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  report(misc + 1);
   if (warp == kWarpMma) {
     __syncwarp();
     tmem_dealloc(tbase, 512);
+  }
+}
+
+// delta = do . o of the queries of samples with more than one key tile (see dq_elementwise).  D / 8
+// lanes per row and four rows per lane, so that a warp has 4 KB in flight; bound by the bytes of o
+// and do.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) cross_delta_kernel(const CrossParams p) {
+  constexpr int LPR = D / 8, ROWS = 4 * 256 / LPR;     // rows of a block: heads of consecutive queries
+  const int64_t first = (int64_t)blockIdx.x * ROWS + threadIdx.x / LPR, total = (int64_t)p.nq * p.heads;
+  const int c = threadIdx.x % LPR * 8;
+  for (int b = blockIdx.y; b < p.batch; b += gridDim.y) {
+    if (cross_len(p, b) <= 128) continue;
+    uint4 a[4] = {}, g[4] = {};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t r = first + i * (256 / LPR);
+      if (r >= total) break;
+      const uint32_t tok = p.div_h.div((uint32_t)r), h = (uint32_t)r - tok * p.heads;
+      a[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.o) + b * p.o_st[0] + tok * p.o_st[1] + h * p.o_st[2] + c));
+      g[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.d_o) + b * p.do_st[0] + tok * p.do_st[1] + h * p.do_st[2] + c));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const T* av = reinterpret_cast<const T*>(&a[i]);
+      const T* gv = reinterpret_cast<const T*>(&g[i]);
+      float s = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s += to_f32(av[e]) * to_f32(gv[e]);
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      const int64_t r = first + i * (256 / LPR);
+      if (c == 0 && r < total) {
+        const uint32_t tok = p.div_h.div((uint32_t)r), h = (uint32_t)r - tok * p.heads;
+        p.delta[((int64_t)b * p.heads + h) * p.nq + tok] = s;
+      }
+    }
   }
 }
 
@@ -583,19 +597,19 @@ struct ItemK {
   int b, hk, kt, split, len, q0, q1;
   __device__ __forceinline__ ItemK(const CrossParams& p, int it) {
     const uint32_t nkt = (p.ns + 127) >> 7;
-    uint32_t i = (uint32_t)it / nkt, u = i;
+    uint32_t i = p.div_kt.div(it), u = i;
     kt = it - i * nkt;
     split = 0;
     if (p.nsplit > 1) {
-      u = i / (uint32_t)p.nsplit;
+      u = p.div_split.div(i);
       split = i - u * p.nsplit;
     }
-    b = u / p.kv_heads;
+    b = p.div_kv.div(u);
     hk = u - b * p.kv_heads;
     len = cross_len(p, b);
     // (fewer than 2^24 query tiles, at most 64 splits: 32 bits hold the products)
-    q0 = split ? (uint32_t)p.nqt * split / (uint32_t)p.nsplit : 0;
-    q1 = kt * 128 < len ? (split + 1 < p.nsplit ? (uint32_t)p.nqt * (split + 1) / (uint32_t)p.nsplit : p.nqt) : q0;
+    q0 = p.div_split.div((uint32_t)p.nqt * split);
+    q1 = kt * 128 < len ? (int)p.div_split.div((uint32_t)p.nqt * (split + 1)) : q0;
   }
 };
 
@@ -610,36 +624,32 @@ __device__ void dkv_producer(const CrossMaps& m, const CrossParams& p, uint32_t 
   bool ok = true;
   for (int it = blockIdx.x; ok && it < p.total; it += gridDim.x) {
     const ItemK w(p, it);
-    for (int i = w.q0; i < w.q1; ++i) {
-      if (i == w.q0) {
-        if (!(ok = wait(C::B_KE, rk.phase() ^ 1))) break;
-        mbar_expect_tx(bar + 8 * C::B_KF, C::TILE);
+    const int q0 = uniform(w.q0), q1 = uniform(w.q1);
+    for (int i = q0; i < q1; ++i) {
+      if (i == q0) {
+        if (!(ok = wait.warp(C::B_KE, rk.phase() ^ 1))) break;
+        mbar_expect_tx_elect(bar + 8 * C::B_KF, C::TILE);
         load_tile<D>(sbase, &m.k, w.kt * 128, w.hk, w.b, bar + 8 * C::B_KF);
         ++rk.n;
       }
       const uint32_t qs = rq.slot(), os = ro.slot();
-      if (!(ok = wait(C::B_QE + qs, rq.phase() ^ 1))) break;
-      mbar_expect_tx(bar + 8 * (C::B_QF + qs), q_bytes);
+      if (!(ok = wait.warp(C::B_QE + qs, rq.phase() ^ 1))) break;
+      mbar_expect_tx_elect(bar + 8 * (C::B_QF + qs), q_bytes);
       load_tile<D>(sbase + C::Q_OFF + qs * C::TILE, &m.q, i * p.toks, w.hk, w.b, bar + 8 * (C::B_QF + qs));
       ++rq.n;
-      if (i == w.q0) {
-        if (!(ok = wait(C::B_VE, rv.phase() ^ 1))) break;
-        mbar_expect_tx(bar + 8 * C::B_VF, C::TILE);
+      if (i == q0) {
+        if (!(ok = wait.warp(C::B_VE, rv.phase() ^ 1))) break;
+        mbar_expect_tx_elect(bar + 8 * C::B_VF, C::TILE);
         load_tile<D>(sbase + C::V_OFF, &m.v, w.kt * 128, w.hk, w.b, bar + 8 * C::B_VF);
         ++rv.n;
       }
-      if (!(ok = wait(C::B_OE + os, ro.phase() ^ 1))) break;
-      mbar_expect_tx(bar + 8 * (C::B_OF + os), q_bytes);
+      if (!(ok = wait.warp(C::B_OE + os, ro.phase() ^ 1))) break;
+      mbar_expect_tx_elect(bar + 8 * (C::B_OF + os), q_bytes);
       load_tile<D>(sbase + C::DO_OFF + os * C::TILE, &m.d_o, i * p.toks, w.hk, w.b, bar + 8 * (C::B_OF + os));
       ++ro.n;
     }
   }
-  if (!ok) {
-    drain_ring(wait, C::B_KF, rk);
-    drain_ring(wait, C::B_VF, rv);
-    drain_ring(wait, C::B_QF, rq);
-    drain_ring(wait, C::B_OF, ro);
-  }
+  if (!ok) settle();
 }
 
 // The rows' constants, four rows a lane, fetched two steps before they are stored: a step is shorter
@@ -655,7 +665,7 @@ __device__ void dkv_rows(const CrossParams& p, float* aux, const Waiter& wait) {
     Rows v;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int r = lane + 32 * k, tr = r / p.group, tok = i * p.toks + tr, h = w.hk * p.group + r - tr * p.group;
+      const int r = lane + 32 * k, tr = row_tok(p, r), tok = i * p.toks + tr, h = w.hk * p.group + r - tr * p.group;
       v.nl[k] = neg_inf();
       v.nd[k] = 0.f;
       if (i < w.q1 && tr < p.toks && tok < p.nq) {
@@ -696,31 +706,32 @@ __device__ void dkv_mma(const CrossParams& p, uint32_t sbase, uint32_t tbase, co
   uint32_t g = 0, items = 0;
   bool ok = true, pending = false, pfirst = false, plast = false;
   uint32_t pq = 0, po = 0, pitem = 0;
-  // dV += P^T dO and dK += dS^T Q of step g - 1
-  auto accumulate = [&]() {
-    if (!wait.warp(C::B_DS, (g - 1) & 1)) return false;
-    if (pfirst && pitem > 0 && !wait.warp(C::B_AE, (pitem - 1) & 1)) return false;
-    tc_fence_after();
-    mma_accum<T, D>(tV, tbase + 128, sbase + C::DO_OFF + po * C::TILE, pfirst);
-    mma_commit_elect(bar + 8 * (C::B_OE + po));
-    mma_accum<T, D>(tK, tbase + 160, sbase + C::Q_OFF + pq * C::TILE, pfirst);
-    mma_commit_elect(bar + 8 * (C::B_QE + pq));
-    if (plast) mma_commit_elect(bar + 8 * C::B_AF);
-    return true;
-  };
-  for (int it = blockIdx.x; ok && it < p.total; it += gridDim.x) {
-    const ItemK w(p, it);
-    const int q0 = uniform(w.q0), q1 = uniform(w.q1);
+  for (int it = blockIdx.x; ok; it += gridDim.x) {      // (one round more: the last step's products)
+    const bool end = it >= p.total;
+    const ItemK w(p, end ? 0 : it);
+    const int q0 = uniform(w.q0), q1 = end ? q0 + 1 : uniform(w.q1);
     for (int i = q0; i < q1; ++i) {
       const bool first = i == q0, last = i == q1 - 1;
-      if (first && !(ok = wait.warp(C::B_KF, rk.phase()))) break;
-      if (!(ok = wait.warp(C::B_QF + rq.slot(), rq.phase()))) break;
-      if (g > 0 && !(ok = wait.warp(C::B_SR, (g - 1) & 1))) break;
-      tc_fence_after();
-      mma_scores<T, D>(tbase, sbase, sbase + C::Q_OFF + rq.slot() * C::TILE);
-      mma_commit_elect(bar + 8 * C::B_SF);
-      if (last) mma_commit_elect(bar + 8 * C::B_KE);
-      if (pending && !(ok = accumulate())) break;
+      if (!end) {
+        if (first && !(ok = wait.warp(C::B_KF, rk.phase()))) break;
+        if (!(ok = wait.warp(C::B_QF + rq.slot(), rq.phase()))) break;
+        if (g > 0 && !(ok = wait.warp(C::B_SR, (g - 1) & 1))) break;
+        tc_fence_after();
+        mma_scores<T, D>(tbase, sbase, sbase + C::Q_OFF + rq.slot() * C::TILE);
+        mma_commit_elect(bar + 8 * C::B_SF);
+        if (last) mma_commit_elect(bar + 8 * C::B_KE);
+      }
+      if (pending) {                   // dV += P^T dO and dK += dS^T Q of step g - 1
+        if (!(ok = wait.warp(C::B_DS, (g - 1) & 1))) break;
+        if (pfirst && pitem > 0 && !(ok = wait.warp(C::B_AE, (pitem - 1) & 1))) break;
+        tc_fence_after();
+        mma_accum<T, D>(tV, tbase + 128, sbase + C::DO_OFF + po * C::TILE, pfirst);
+        mma_commit_elect(bar + 8 * (C::B_OE + po));
+        mma_accum<T, D>(tK, tbase + 160, sbase + C::Q_OFF + pq * C::TILE, pfirst);
+        mma_commit_elect(bar + 8 * (C::B_QE + pq));
+        if (plast) mma_commit_elect(bar + 8 * C::B_AF);
+      }
+      if (end) return;
       if (first && !(ok = wait.warp(C::B_VF, rk.phase()))) break;
       if (!(ok = wait.warp(C::B_OF + ro.slot(), ro.phase()))) break;
       tc_fence_after();
@@ -743,11 +754,8 @@ __device__ void dkv_mma(const CrossParams& p, uint32_t sbase, uint32_t tbase, co
       ++items;
     }
   }
-  if (ok && pending) ok = accumulate();
-  if (!ok) {
-    mma_commit_elect(bar + 8 * C::B_DRAIN);
-    wait.drain(C::B_DRAIN, 0);
-  }
+  mma_commit_elect(bar + 8 * C::B_DRAIN);
+  wait.drain(C::B_DRAIN, 0);
 }
 
 template <typename T, int D>
@@ -762,103 +770,103 @@ __device__ void dkv_elementwise(const CrossParams& p, const float* aux, uint32_t
   Ring<C::NA> ra;
   T *pend_k = nullptr, *pend_v = nullptr;
   float* pend_part = nullptr;
-  bool pending = false, pend_vis = false;
-  // the accumulators of the item before: dV, dK rows, or their fp32 partials [2][128][D]
-  auto finish = [&]() {
-    if (!wait.warp(C::B_AF, (items - 1) & 1)) return false;
-    tc_fence_after();
-    if (p.part) {
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int ch = 0; ch < D / 64; ++ch) {
-          uint32_t o[32];
-          __syncwarp();
-          tmem_ld32_sync(tAcc + t * D + ch * 32, o);
-          if (!pend_vis) continue;
-          uint4* dst = reinterpret_cast<uint4*>(pend_part + t * 128 * D + ch * 32);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) dst[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
-        }
-    } else {
-      store_half<T, D>(tAcc, pend_vis ? pend_v : nullptr, 1.0f);
-      store_half<T, D>(tAcc + D, pend_vis ? pend_k : nullptr, p.scale);
-    }
-    tc_fence_before();
-    warp_arrive(bar + 8 * C::B_AE);
-    pending = false;
-    return true;
-  };
-  for (int it = blockIdx.x; it < p.total; it += gridDim.x) {
-    const ItemK w(p, it);
+  bool pend_vis = false;
+  for (int it = blockIdx.x;; it += gridDim.x) {
+    const bool end = it >= p.total;    // one round more: the last item's accumulators
+    if (end && items == 0) return;
+    const ItemK w(p, end ? 0 : it);
     const int key = w.kt * 128 + r;
     const uint4 words = cross_words(p, w.b, w.kt, w.len);
     const bool vis = (word_of(words, r >> 5) >> (r & 31)) & 1u;
     T* out_k = static_cast<T*>(p.out[0]) + w.b * p.out_st[0][0] + key * p.out_st[0][1] + w.hk * p.out_st[0][2] + half * (D / 2);
     T* out_v = static_cast<T*>(p.out[1]) + w.b * p.out_st[1][0] + key * p.out_st[1][1] + w.hk * p.out_st[1][2] + half * (D / 2);
-    if (!p.part && key < p.ns && !vis) {       // (with partials the join writes these)
+    if (!end && !p.part && key < p.ns && !vis) {       // (with partials the join writes these)
       zero_half<T, D>(out_k);
       zero_half<T, D>(out_v);
     }
-    if (w.q1 == w.q0) continue;
+    if (!end && w.q1 == w.q0) continue;
     const bool zero = w.len == 1 || (p.single && __ldg(p.single + w.b));
-    for (int i = w.q0; i < w.q1; ++i) {
-      uint32_t s[64];
-      const float4* nl = reinterpret_cast<const float4*>(aux + ra.slot() * 256 + half * 64);
-      if (!wait.warp(C::B_XF + ra.slot(), ra.phase())) return;
-      if (!wait.warp(C::B_SF, g & 1)) return;
-      tc_fence_after();
-      tmem_ld64_sync(tS, s);
-      tc_fence_before();
-      warp_arrive(bar + 8 * C::B_SR);
-      uint32_t pk[32], dk[32];
+    for (int i = w.q0; i < (end ? w.q0 + 1 : w.q1); ++i) {
+      if (!end) {
+        uint32_t s[64];
+        const float4* nl = reinterpret_cast<const float4*>(aux + ra.slot() * 256 + half * 64);
+        if (!wait.warp(C::B_XF + ra.slot(), ra.phase())) return;
+        if (!wait.warp(C::B_SF, g & 1)) return;
+        tc_fence_after();
+        tmem_ld64_sync(tS, s);
+        tc_fence_before();
+        warp_arrive(bar + 8 * C::B_SR);
+        uint32_t pk[32], dk[32];
 #pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        const float4 l = nl[c];
-        const float2 a = ffma2(make_float2(__uint_as_float(s[4 * c]), __uint_as_float(s[4 * c + 1])), scale2, make_float2(l.x, l.y));
-        const float2 b = ffma2(make_float2(__uint_as_float(s[4 * c + 2]), __uint_as_float(s[4 * c + 3])), scale2, make_float2(l.z, l.w));
-        s[4 * c] = __float_as_uint(ex2(a.x));
-        s[4 * c + 1] = __float_as_uint(ex2(a.y));
-        s[4 * c + 2] = __float_as_uint(ex2(b.x));
-        s[4 * c + 3] = __float_as_uint(ex2(b.y));
-        pk[2 * c] = vis ? pack2<T>(__uint_as_float(s[4 * c]), __uint_as_float(s[4 * c + 1])) : 0u;
-        pk[2 * c + 1] = vis ? pack2<T>(__uint_as_float(s[4 * c + 2]), __uint_as_float(s[4 * c + 3])) : 0u;
-      }
-      if (!wait.warp(C::B_PF, g & 1)) return;
-      tc_fence_after();
-      const float4* nd = nl + 32;
-      uint32_t d[64];
-      tmem_ld64_sync(tP, d);
-      tmem_st32(tP, pk);
+        for (int c = 0; c < 16; ++c) {
+          const float4 l = nl[c];
+          const float2 a = ffma2(make_float2(__uint_as_float(s[4 * c]), __uint_as_float(s[4 * c + 1])), scale2, make_float2(l.x, l.y));
+          const float2 b = ffma2(make_float2(__uint_as_float(s[4 * c + 2]), __uint_as_float(s[4 * c + 3])), scale2, make_float2(l.z, l.w));
+          s[4 * c] = __float_as_uint(ex2(a.x));
+          s[4 * c + 1] = __float_as_uint(ex2(a.y));
+          s[4 * c + 2] = __float_as_uint(ex2(b.x));
+          s[4 * c + 3] = __float_as_uint(ex2(b.y));
+          pk[2 * c] = vis ? pack2<T>(__uint_as_float(s[4 * c]), __uint_as_float(s[4 * c + 1])) : 0u;
+          pk[2 * c + 1] = vis ? pack2<T>(__uint_as_float(s[4 * c + 2]), __uint_as_float(s[4 * c + 3])) : 0u;
+        }
+        if (!wait.warp(C::B_PF, g & 1)) return;
+        tc_fence_after();
+        const float4* nd = nl + 32;
+        uint32_t d[64];
+        tmem_ld64_sync(tP, d);
+        tmem_st32(tP, pk);
 #pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        const float4 l = nd[c];
-        const int k = 4 * c;
-        const float2 a = fmul2(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])),
-                               fadd2(make_float2(__uint_as_float(d[k]), __uint_as_float(d[k + 1])), make_float2(l.x, l.y)));
-        const float2 b = fmul2(make_float2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])),
-                               fadd2(make_float2(__uint_as_float(d[k + 2]), __uint_as_float(d[k + 3])), make_float2(l.z, l.w)));
-        dk[2 * c] = vis && !zero ? pack2<T>(a.x, a.y) : 0u;
-        dk[2 * c + 1] = vis && !zero ? pack2<T>(b.x, b.y) : 0u;
+        for (int c = 0; c < 16; ++c) {
+          const float4 l = nd[c];
+          const int k = 4 * c;
+          const float2 a = fmul2(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])),
+                                 fadd2(make_float2(__uint_as_float(d[k]), __uint_as_float(d[k + 1])), make_float2(l.x, l.y)));
+          const float2 b = fmul2(make_float2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])),
+                                 fadd2(make_float2(__uint_as_float(d[k + 2]), __uint_as_float(d[k + 3])), make_float2(l.z, l.w)));
+          dk[2 * c] = vis && !zero ? pack2<T>(a.x, a.y) : 0u;
+          dk[2 * c + 1] = vis && !zero ? pack2<T>(b.x, b.y) : 0u;
+        }
+        __syncwarp();
+        tmem_st32(tP + 32, dk);
+        tmem_wait_st();
+        tc_fence_before();
+        warp_arrive(bar + 8 * C::B_DS);
+        warp_arrive(bar + 8 * (C::B_XE + ra.slot()));
+        ++ra.n;
+        ++g;
       }
-      __syncwarp();
-      tmem_st32(tP + 32, dk);
-      tmem_wait_st();
-      tc_fence_before();
-      warp_arrive(bar + 8 * C::B_DS);
-      warp_arrive(bar + 8 * (C::B_XE + ra.slot()));
-      ++ra.n;
-      ++g;
-      if (pending && !finish()) return;
+      // the accumulators of the item before: dV, dK rows, or their fp32 partials [2][128][D]
+      if (i == w.q0 && items > 0) {
+        if (!wait.warp(C::B_AF, (items - 1) & 1)) return;
+        tc_fence_after();
+        if (p.part) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int ch = 0; ch < D / 64; ++ch) {
+              uint32_t o[32];
+              __syncwarp();
+              tmem_ld32_sync(tAcc + t * D + ch * 32, o);
+              if (!pend_vis) continue;
+              uint4* dst = reinterpret_cast<uint4*>(pend_part + t * 128 * D + ch * 32);
+#pragma unroll
+              for (int q = 0; q < 8; ++q) dst[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            }
+        } else {
+          store_piece<T, D / 2>(tAcc, pend_vis ? pend_v : nullptr, 1.0f);
+          store_piece<T, D / 2>(tAcc + D, pend_vis ? pend_k : nullptr, p.scale);
+        }
+        tc_fence_before();
+        warp_arrive(bar + 8 * C::B_AE);
+      }
     }
+    if (end) return;
     ++items;
-    pending = true;
     pend_k = out_k;
     pend_v = out_v;
     pend_vis = vis;
     if (p.part) pend_part = p.part + ((int64_t)it * 2 * 128 + r) * D + half * (D / 2);
   }
-  if (pending) finish();
 }
 
 template <typename T, int D>
@@ -871,13 +879,12 @@ __global__ void __launch_bounds__(kThreadsK, 1) cross_dkv_kernel(const __grid_co
     return;
   }
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
   const uint32_t bar = sbase + C::BAR_OFF;
   float* aux = reinterpret_cast<float*>(smem + C::AUX_OFF);
-  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5);
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NBAR; ++i) mbar_init(bar + 8 * i, C::arrivals(i));
-    *abort_flag = 0;
+    misc[1] = 0;                       // abort word
     fence_mbar_init();
   }
   if (p.toks * p.group < 128) {
@@ -893,12 +900,12 @@ __global__ void __launch_bounds__(kThreadsK, 1) cross_dkv_kernel(const __grid_co
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = misc[0];
-  Waiter wait{bar, abort_flag, DEV_TIMEOUT_SOFTMAX, p.timeout_ns};
+  Waiter wait{bar, smem_u32(misc + 1), DEV_TIMEOUT_SOFTMAX, (uint32_t)p.timeout_ns};
   if (warp >= 8) {
     regs_shrink<kRegsOtherK>();
     if (warp == kWarpProducer) {
       wait.code = DEV_TIMEOUT_PRODUCER;
-      if (lane == 0) dkv_producer<D>(m, p, sbase, wait);
+      dkv_producer<D>(m, p, sbase, wait);
     } else if (warp == kWarpMma) {
       wait.code = DEV_TIMEOUT_MMA;
       dkv_mma<T, D>(p, sbase, uniform(tbase), wait);
@@ -912,6 +919,7 @@ __global__ void __launch_bounds__(kThreadsK, 1) cross_dkv_kernel(const __grid_co
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  report(misc + 1);
   if (warp == kWarpMma) {
     __syncwarp();
     tmem_dealloc(tbase, 512);
@@ -972,6 +980,11 @@ template <typename T, int D> struct TagK {};
 
 template <typename T, int D>
 cudaError_t launch_dq(const CrossMaps& m, const CrossParams& p, int grid, cudaStream_t s) {
+  if (p.ns > 128) {
+    constexpr int kRows = 4 * 256 / (D / 8);
+    const dim3 blocks((unsigned)(((int64_t)p.nq * p.heads + kRows - 1) / kRows), std::min(p.batch, 65535));
+    cross_delta_kernel<T, D><<<blocks, 256, 0, s>>>(p);
+  }
   return launch<TagQ<T, D>>(cross_dq_kernel<T, D>, kRegsLaunchQ, kThreadsQ, CfgQ<D>::SMEM, m, p, grid, s);
 }
 template <typename T, int D>

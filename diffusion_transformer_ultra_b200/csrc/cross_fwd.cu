@@ -60,12 +60,12 @@ struct Item {
     uint32_t i = it, u;
     split = 0;
     if (p.nsplit > 1) {
-      split = i % p.nsplit;
-      i /= p.nsplit;
+      i = p.div_split.div(it);
+      split = it - i * p.nsplit;
     }
-    u = i / p.nitem_q;
+    u = p.div_q.div(i);
     qt0 = (i - u * p.nitem_q) * p.per_item;
-    b = u / p.kv_heads;
+    b = p.div_kv.div(u);
     hk = u - b * p.kv_heads;
     ntile = min(p.per_item, p.nqt - qt0);
     len = cross_len(p, b);
@@ -257,7 +257,7 @@ __device__ void softmax_role(const CrossParams& p, uint8_t* smem, uint32_t sbase
   const uint32_t tS = tbase + lane_off + (uint32_t)(t * 128);
   const uint32_t tO = tbase + lane_off + C::O_COL + (uint32_t)(t * D);
   const float scale = p.scale_log2;
-  const int tok_r = r / p.group, g_r = r - tok_r * p.group;
+  const int tok_r = row_tok(p, r), g_r = r - tok_r * p.group;
   uint8_t* out = smem + C::OUT_OFF + (threadIdx.x >> 5) * 4096;
   uint32_t sc = 0, oc = 0;
   for (int it = blockIdx.x; it < p.total; it += gridDim.x) {

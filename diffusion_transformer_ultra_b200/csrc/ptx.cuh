@@ -94,6 +94,36 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
+// The same wait in few instructions, for kernels whose roles together outgrow the instruction cache
+// (every wait's code is fetched along with the code around it): the CTA's abort word in shared memory
+// holds the code of the first wait that ran out, which the kernel reports when it ends.  `limit_ns` <
+// 2^31 (the 32-bit timer wraps after 4.3 s).
+__device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, uint32_t abort_word, int code, uint32_t limit_ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 t0, t, f;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %6;\n\t"
+      "mov.u32 %0, 1;\n\t"
+      "@p bra DONE_%=;\n\t"
+      "mov.u32 t0, %%globaltimer_lo;\n"
+      "LOOP_%=:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %6;\n\t"
+      "@p bra DONE_%=;\n\t"
+      "ld.volatile.shared.u32 f, [%3];\n\t"
+      "mov.u32 t, %%globaltimer_lo;\n\t"
+      "sub.u32 t, t, t0;\n\t"
+      "setp.gt.u32 q, t, %5;\n\t"
+      "@q st.volatile.shared.u32 [%3], %4;\n\t"
+      "setp.ne.or.u32 q, f, 0, q;\n\t"
+      "@!q bra LOOP_%=;\n\t"
+      "mov.u32 %0, 0;\n"
+      "DONE_%=:\n\t}"
+      : "=&r"(ok)
+      : "r"(bar), "r"(parity), "r"(abort_word), "r"(code), "r"(limit_ns), "r"(20000)
+      : "memory");
+  return ok != 0;
+}
+
 // 2^x on the SFU (ex2.approx.ftz.f32): 2^-inf = +0.
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -172,11 +202,30 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const void* tmap, int 
       : "memory");
 }
 
+// The same from a converged warp, by its elected lane.
+__device__ __forceinline__ void tma_load_5d_elect(uint32_t dst, const void* tmap, int c0, int c1, int c2, int c3, int c4,
+                                                  uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_expect_tx_elect(uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t.reg .b64 s;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q mbarrier.arrive.expect_tx.shared::cta.b64 s, [%0], %1;\n\t}" ::"r"(bar),
+      "r"(bytes)
+      : "memory");
+}
 // The tile into L2 only.
-__device__ __forceinline__ void tma_prefetch_5d(const void* tmap, int c0, int c1, int c2, int c3, int c4) {
-  asm volatile("cp.async.bulk.prefetch.tensor.5d.L2.global [%0, {%1, %2, %3, %4, %5}];" ::"l"(reinterpret_cast<uint64_t>(tmap)),
-               "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
-               : "memory");
+__device__ __forceinline__ void tma_prefetch_5d_elect(const void* tmap, int c0, int c1, int c2, int c3, int c4) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q cp.async.bulk.prefetch.tensor.5d.L2.global [%0, {%1, %2, %3, %4, %5}];\n\t}" ::"l"(reinterpret_cast<uint64_t>(tmap)),
+      "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+      : "memory");
 }
 
 // ---------------------------------------------------------------- tcgen05
@@ -289,6 +338,77 @@ __device__ __forceinline__ void mma_ts_elect(uint32_t d_tmem, uint32_t a_tmem, u
       "setp.ne.b32 p, %5, 0;\n\t"
       "mov.b64 bd, {%2, %3};\n\t"
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], bd, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// All products of a [128 x 128] = A B^T over K = D, both [128 x D] tiles K-major in 128-byte swizzled
+// boxes of 64 elements, 16 KB each: one elect, the offsets as immediates.
+template <int D>
+__device__ __forceinline__ void mma_ss_tile_elect(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc) {
+  static_assert(D == 64 || D == 128, "");
+  if constexpr (D == 128)
+    asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 ad, bd;\n\t.reg .b32 a, b;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, 0, 0;\n\t"
+      "mov.b64 ad, {%1, %3};\n\tmov.b64 bd, {%2, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %4, p;\n\tsetp.eq.b32 p, 0, 0;\n\t"
+      "add.u32 a, %1, 2;\n\tadd.u32 b, %2, 2;\n\tmov.b64 ad, {a, %3};\n\tmov.b64 bd, {b, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %4, p;\n\t"
+      "add.u32 a, %1, 4;\n\tadd.u32 b, %2, 4;\n\tmov.b64 ad, {a, %3};\n\tmov.b64 bd, {b, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %4, p;\n\t"
+      "add.u32 a, %1, 6;\n\tadd.u32 b, %2, 6;\n\tmov.b64 ad, {a, %3};\n\tmov.b64 bd, {b, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %4, p;\n\t"
+      "add.u32 a, %1, 1024;\n\tadd.u32 b, %2, 1024;\n\tmov.b64 ad, {a, %3};\n\tmov.b64 bd, {b, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %4, p;\n\t"
+      "add.u32 a, %1, 1026;\n\tadd.u32 b, %2, 1026;\n\tmov.b64 ad, {a, %3};\n\tmov.b64 bd, {b, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %4, p;\n\t"
+      "add.u32 a, %1, 1028;\n\tadd.u32 b, %2, 1028;\n\tmov.b64 ad, {a, %3};\n\tmov.b64 bd, {b, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %4, p;\n\t"
+      "add.u32 a, %1, 1030;\n\tadd.u32 b, %2, 1030;\n\tmov.b64 ad, {a, %3};\n\tmov.b64 bd, {b, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %4, p;\n\t"
+      "}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc)
+        : "memory");
+  else
+    asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 ad, bd;\n\t.reg .b32 a, b;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, 0, 0;\n\t"
+      "mov.b64 ad, {%1, %3};\n\tmov.b64 bd, {%2, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %4, p;\n\tsetp.eq.b32 p, 0, 0;\n\t"
+      "add.u32 a, %1, 2;\n\tadd.u32 b, %2, 2;\n\tmov.b64 ad, {a, %3};\n\tmov.b64 bd, {b, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %4, p;\n\t"
+      "add.u32 a, %1, 4;\n\tadd.u32 b, %2, 4;\n\tmov.b64 ad, {a, %3};\n\tmov.b64 bd, {b, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %4, p;\n\t"
+      "add.u32 a, %1, 6;\n\tadd.u32 b, %2, 6;\n\tmov.b64 ad, {a, %3};\n\tmov.b64 bd, {b, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %4, p;\n\t"
+      "}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc)
+        : "memory");
+}
+// All products of [128 x N] (+)= A B over K = 128: A packed 16-bit in TMEM, columns 64 h .. 64 h + 63 of
+// it at column a + 64 h; B MN-major.  accumulate = 0 replaces D.
+__device__ __forceinline__ void mma_ts_tile_elect(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t hi, uint32_t idesc,
+                                                  uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 bd;\n\t.reg .b32 a, b;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 bd, {%2, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], bd, %4, p;\n\tsetp.eq.b32 p, 0, 0;\n\t"
+      "add.u32 a, %1, 8;\n\tadd.u32 b, %2, 128;\n\tmov.b64 bd, {b, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], bd, %4, p;\n\t"
+      "add.u32 a, %1, 16;\n\tadd.u32 b, %2, 256;\n\tmov.b64 bd, {b, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], bd, %4, p;\n\t"
+      "add.u32 a, %1, 24;\n\tadd.u32 b, %2, 384;\n\tmov.b64 bd, {b, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], bd, %4, p;\n\t"
+      "add.u32 a, %1, 64;\n\tadd.u32 b, %2, 512;\n\tmov.b64 bd, {b, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], bd, %4, p;\n\t"
+      "add.u32 a, %1, 72;\n\tadd.u32 b, %2, 640;\n\tmov.b64 bd, {b, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], bd, %4, p;\n\t"
+      "add.u32 a, %1, 80;\n\tadd.u32 b, %2, 768;\n\tmov.b64 bd, {b, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], bd, %4, p;\n\t"
+      "add.u32 a, %1, 88;\n\tadd.u32 b, %2, 896;\n\tmov.b64 bd, {b, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], bd, %4, p;\n\t"
+      "}" ::"r"(d_tmem),
       "r"(a_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
