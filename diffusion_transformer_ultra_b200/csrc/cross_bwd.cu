@@ -26,8 +26,6 @@ namespace {
 __device__ int g_error;                // first wait that ran out since the last status read
 
 constexpr int kWarpProducer = 8, kWarpMma = 9, kWarpAux = 10;
-constexpr uint64_t kDrainNs = 50ull * 1000 * 1000;   // bounded drain on the abort path
-constexpr int BOX_BYTES = 128 * 64 * 2;
 
 // Slot and wait parity of the n-th use of a ring of N slots.
 template <int N>
@@ -37,104 +35,10 @@ struct Ring {
   __device__ __forceinline__ uint32_t phase() const { return (n / N) & 1; }
 };
 
-struct Waiter {
-  uint32_t bar;                        // first barrier
-  uint32_t abort_word;
-  int code;
-  uint32_t limit_ns;
-  __device__ __forceinline__ bool operator()(int b, uint32_t parity) const {
-    return mbar_wait_short(bar + 8 * b, parity, abort_word, code, limit_ns);
-  }
-  // all lanes of the warp
-  __device__ __forceinline__ bool warp(int b, uint32_t parity) const {
-    return __all_sync(0xffffffffu, (*this)(b, parity));
-  }
-  __device__ __forceinline__ void drain(int b, uint32_t parity) const {
-    mbar_wait(bar + 8 * b, parity, nullptr, &g_error, DEV_TIMEOUT_DRAIN, kDrainNs);
-  }
-};
-
 // At a kernel's end: a wait that ran out.
 __device__ __forceinline__ void report(const uint32_t* abort_word) {
   const int code = *reinterpret_cast<const volatile int*>(abort_word);
   if (threadIdx.x == 0 && code != 0) atomicExch(&g_error, code);
-}
-
-// After a wait that ran out: the copies in flight land well within this time, and none may land after
-// this CTA exits.
-__device__ __noinline__ void settle() {
-  const uint64_t t0 = globaltimer_ns();
-  while (globaltimer_ns() - t0 < kDrainNs) __nanosleep(1000);
-}
-
-__device__ __forceinline__ void warp_arrive(uint32_t bar) {
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
-}
-
-// One [128 x D] tile: D / 64 boxes of 64 elements.  `head_row`: the row coordinate.
-template <int D>
-__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* m, int row, int hk, int b, uint32_t bar) {
-#pragma unroll
-  for (int bx = 0; bx < D / 64; ++bx) tma_load_5d_elect(dst + bx * BOX_BYTES, m, bx * 64, 0, row, hk, b, bar);
-}
-
-// D[128 x 128] = A B^T over K = D, both tiles K-major.
-template <typename T, int D>
-__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b) {
-  mma_ss_tile_elect<D>(d, desc_lo(a, 16), desc_lo(b, 16), desc_hi_sw128(1024), idesc_half<T>(128, 128, 0));
-}
-
-// D[128 x D] (+)= A B: A a packed 16-bit operand in TMEM, B a [128 x D] tile read MN-major.
-template <typename T, int D>
-__device__ __forceinline__ void mma_accum(uint32_t d, uint32_t a, uint32_t b, bool first) {
-  mma_ts_tile_elect(d, a, desc_lo(b, BOX_BYTES), desc_hi_sw128(1024), idesc_half<T>(128, D, 1), first ? 0u : 1u);
-}
-
-// W columns of a row of an accumulator per lane, scaled and rounded, to 16-bit global memory.  Stores
-// by row would go to 32 rows each; N = W / 8 lanes exchange their 16-byte pieces first (a transpose of
-// N x N pieces in log2(N) rounds), so that N lanes write one row's 2 W bytes together.  `row` is the
-// lane's destination, null for a row that is not stored.
-template <typename T, int W>
-__device__ __forceinline__ void store_piece(uint32_t tmem, T* row, float f) {
-  constexpr int N = W / 8;
-  const int lane = threadIdx.x & 31, c = lane & (N - 1);
-  uint4 v[N];
-  {
-    uint32_t o[W];
-    __syncwarp();
-    if constexpr (W == 64) tmem_ld64_sync(tmem, o);
-    else tmem_ld32_sync(tmem, o);
-#pragma unroll
-    for (int q = 0; q < N; ++q) {
-      v[q].x = pack2<T>(__uint_as_float(o[8 * q + 0]) * f, __uint_as_float(o[8 * q + 1]) * f);
-      v[q].y = pack2<T>(__uint_as_float(o[8 * q + 2]) * f, __uint_as_float(o[8 * q + 3]) * f);
-      v[q].z = pack2<T>(__uint_as_float(o[8 * q + 4]) * f, __uint_as_float(o[8 * q + 5]) * f);
-      v[q].w = pack2<T>(__uint_as_float(o[8 * q + 6]) * f, __uint_as_float(o[8 * q + 7]) * f);
-    }
-  }
-#pragma unroll
-  for (int b = 1; b < N; b *= 2) {
-    const bool up = lane & b;
-#pragma unroll
-    for (int q = 0; q < N; ++q) {
-      if (q & b) continue;
-      uint4 &lo = v[q], &hi = v[q | b];
-      uint4 t = up ? lo : hi;
-      t.x = __shfl_xor_sync(0xffffffffu, t.x, b);
-      t.y = __shfl_xor_sync(0xffffffffu, t.y, b);
-      t.z = __shfl_xor_sync(0xffffffffu, t.z, b);
-      t.w = __shfl_xor_sync(0xffffffffu, t.w, b);
-      if (up) lo = t;
-      else hi = t;
-    }
-  }
-  // v[q] is now piece c of the row of lane (lane - c + q)
-#pragma unroll
-  for (int q = 0; q < N; ++q) {
-    T* dst = reinterpret_cast<T*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), lane - c + q));
-    if (dst) *reinterpret_cast<uint4*>(dst + c * 8) = v[q];
-  }
 }
 
 template <typename T, int D>
@@ -362,7 +266,7 @@ __device__ void dq_mma(const CrossParams& p, uint32_t sbase, uint32_t tbase, con
     }
   }
   mma_commit_elect(bar + 8 * C::B_DRAIN);
-  wait.drain(C::B_DRAIN, 0);
+  wait.drain(C::B_DRAIN, 0, &g_error);
 }
 
 // The elementwise part.  delta comes from do . o, except where all of a row's keys are in one tile:
@@ -755,7 +659,7 @@ __device__ void dkv_mma(const CrossParams& p, uint32_t sbase, uint32_t tbase, co
     }
   }
   mma_commit_elect(bar + 8 * C::B_DRAIN);
-  wait.drain(C::B_DRAIN, 0);
+  wait.drain(C::B_DRAIN, 0, &g_error);
 }
 
 template <typename T, int D>

@@ -96,8 +96,9 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
 
 // The same wait in few instructions, for kernels whose roles together outgrow the instruction cache
 // (every wait's code is fetched along with the code around it): the CTA's abort word in shared memory
-// holds the code of the first wait that ran out, which the kernel reports when it ends.  `limit_ns` <
-// 2^31 (the 32-bit timer wraps after 4.3 s).
+// holds the code of a wait that ran out, which the kernel reports when it ends.  `limit_ns` < 2^31: the
+// 32-bit timer wraps after 4.3 s, and the difference is taken as signed, so that a timer that steps
+// back a little ends no wait.
 __device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, uint32_t abort_word, int code, uint32_t limit_ns) {
   uint32_t ok;
   asm volatile(
@@ -112,7 +113,7 @@ __device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, u
       "ld.volatile.shared.u32 f, [%3];\n\t"
       "mov.u32 t, %%globaltimer_lo;\n\t"
       "sub.u32 t, t, t0;\n\t"
-      "setp.gt.u32 q, t, %5;\n\t"
+      "setp.gt.s32 q, t, %5;\n\t"
       "@q st.volatile.shared.u32 [%3], %4;\n\t"
       "setp.ne.or.u32 q, f, 0, q;\n\t"
       "@!q bra LOOP_%=;\n\t"
