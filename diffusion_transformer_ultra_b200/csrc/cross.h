@@ -56,6 +56,7 @@ cudaError_t launch_cross_dkv(const CrossMaps& m, const CrossParams& p, int dtype
 // Device error words of the kernels: read and cleared, in stream order; waits for `s`.
 cudaError_t cross_fwd_status(int* code, cudaStream_t s);
 cudaError_t cross_bwd_status(int* code, cudaStream_t s);
+cudaError_t norm_status(int* code, cudaStream_t s);
 // Reads `symbol` (a device int) after the work of `s`, and clears it if it is set.
 cudaError_t read_clear_error(const void* symbol, int* code, cudaStream_t s);
 

@@ -306,9 +306,10 @@ int ultragen_operator_status(ultragen_stream_t stream) {
   int back = 0;
   if ((st = status_of(cross_fwd_status(&code, reinterpret_cast<cudaStream_t>(stream))))) return st;
   if ((st = status_of(cross_bwd_status(&back, reinterpret_cast<cudaStream_t>(stream))))) return st;
-  int proj = 0;
+  int proj = 0, norm = 0;
   if ((st = status_of(adapter_status(&proj, reinterpret_cast<cudaStream_t>(stream))))) return st;
-  return code || back || proj ? ULTRAGEN_ERR_TIMEOUT : ULTRAGEN_OK;
+  if ((st = status_of(norm_status(&norm, reinterpret_cast<cudaStream_t>(stream))))) return st;
+  return code || back || proj || norm ? ULTRAGEN_ERR_TIMEOUT : ULTRAGEN_OK;
 }
 
 int ultragen_cross_attention_backward(const ultragen_cross_t* c, const void* d_o, const void* q, const void* k,

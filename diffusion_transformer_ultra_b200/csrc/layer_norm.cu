@@ -7,11 +7,14 @@
 //   dw = sum over rows of dy xh,   db = sum over rows of dy
 //
 // Both passes are bound by HBM: x is read and y written once (x, dy read and dx written once).
-// A row lives in the registers of its block, kElems elements per thread, so that the variance
-// takes a second pass over registers (no cancellation of sum(x^2) against mu^2) and nothing is
-// read twice.  All sums are fp32.  A row of up to 512 elements belongs to one warp and a block
-// holds several rows; a longer one to a block of just enough warps, so that few lanes idle at
-// any width.
+// A row belongs to one warp up to 2,048 elements of 16 bits (1,024 of 32; the backward pass, which
+// keeps the weight's gradient too, fewer), else to a group of warps.  Its rows come by bulk copies,
+// several ahead, into shared memory (a persistent block per multiprocessor has up to 200 KB of them in
+// flight; with loads straight to registers the forward pass took 132 us, and with a row to a block
+// 151 us, for 70,144 x 2,048 bf16), and from there to registers, as they were read, so that the
+// variance takes a second pass over registers (no cancellation of sum(x^2) against mu^2).  A copy
+// covers the 16-byte pieces that hold the row, so that a row may start anywhere; rows that do not start
+// on 16 bytes are then worked on element by element.  All sums are fp32.
 //
 // The weight's gradient: a block of the backward pass walks a run of rows of one sample (of the
 // whole batch with a shared weight), keeps its columns' sums in registers, and writes them once
@@ -23,19 +26,18 @@
 #include <cmath>
 #include <cstdint>
 
+#include "cross.cuh"
 #include "device.h"
 #include "elem.cuh"
 #include "kernels.h"
 #include "nvtx_range.h"
+#include "ptx.cuh"
 #include "ultragen.h"
 
 namespace ug {
 namespace {
 
-constexpr int kElems = 16;                 // elements of a row per thread
-constexpr int kMaxCols = 16384;            // 1,024 threads of kElems elements
-constexpr int kWarpCols = 32 * kElems;     // rows up to this belong to one warp
-constexpr int kWarpRows = 8;               // rows per block then
+constexpr int kMaxCols = 16384;
 
 struct NormArgs {
   const void* x;
@@ -49,107 +51,202 @@ struct NormArgs {
   int64_t x_row, x_batch, y_row, y_batch, dy_row, dy_batch;
   int64_t total;           // rows of all samples
   int rows, C;             // rows per sample
+  FastDiv div_rows;        // by rows
   int64_t w_batch;         // C with a weight per sample, else 0
   int runs_per_group;      // runs of a sample (of everything with a shared weight)
   int64_t group_rows;      // rows of a sample (of everything with a shared weight)
+  int warps;               // warps of a row
+  int at_once;             // rows of a block at a time
+  int slots, slot_bytes;   // rows in flight per row group; bytes of one tensor's row in a slot
   float plus, inv_c, eps;
 };
 
-// Sum of x over the threads of a row: one warp, or the whole block (two barriers; `red` holds a
-// float per warp and may be reused at once by the next call because of the second).
-template <bool WARP>
-__device__ __forceinline__ float row_sum(float x, float* red) {
-  x = warp_sum(x);
-  if (WARP) return x;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
-  if (lane == 0) red[warp] = x;
+// Threads of a row, and the sums over them: a warp's own, or through shared memory behind a named
+// barrier of the row's warps.  `red` is double-buffered: whoever writes a buffer again has passed the
+// barrier of the sum between, which its readers had to reach first.
+template <bool MULTI>
+struct Row {
+  int t, threads, group;               // this thread's place in the row, threads of a row, row of the block
+  float2* red;                         // [2][32], one entry per warp of the block
+  int flip;
+  __device__ __forceinline__ Row(const NormArgs& p, float2* smem) : red(smem), flip(0) {
+    const int warp = threadIdx.x >> 5;
+    group = MULTI ? warp / p.warps : warp;
+    threads = MULTI ? p.warps * 32 : 32;
+    t = threadIdx.x - group * threads;
+  }
+  __device__ __forceinline__ float2 sum(float2 x, int warps) {
+    x.x = warp_sum(x.x);
+    x.y = warp_sum(x.y);
+    if (!MULTI) return x;
+    const int lane = threadIdx.x & 31;
+    float2* buf = red + flip * 32 + group * warps;
+    flip ^= 1;
+    if (lane == 0) buf[t >> 5] = x;
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(threads) : "memory");
+    x = lane < warps ? buf[lane] : make_float2(0.f, 0.f);
+    x.x = warp_sum(x.x);
+    x.y = warp_sum(x.y);
+    return x;
+  }
+};
+
+__device__ int g_error;                // a wait that ran out since the last status read
+
+constexpr uint32_t kWaitNs = 2000u * 1000 * 1000;
+
+// The rows of one row group on their way through shared memory: `slots` slots of N tensors' rows each.
+template <typename T, int N>
+struct Ring {
+  uint32_t bar, abort_word;            // barriers of this group's slots
+  uint8_t* buf;
+  int slots, slot_bytes, row_bytes, slot;
+  uint32_t phase;
+  __device__ __forceinline__ Ring(const NormArgs& p, int group, uint64_t* bars, uint8_t* smem, uint32_t* abort)
+      : bar(smem_u32(bars + group * p.slots)), abort_word(smem_u32(abort)),
+        buf(smem + (int64_t)group * p.slots * N * p.slot_bytes), slots(p.slots), slot_bytes(p.slot_bytes),
+        row_bytes(p.C * (int)sizeof(T)), slot(0), phase(0) {}
+  // One thread: the 16-byte pieces that hold the rows at src[0 .. N) into slot `to`.
+  __device__ __forceinline__ void issue(int to, const T* const (&src)[N]) const {
+    uint32_t bytes[N], total = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint32_t off = (uint32_t)(uintptr_t)src[i] & 15u;
+      bytes[i] = (off + row_bytes + 15) & ~15u;
+      total += bytes[i];
+    }
+    mbar_expect_tx(bar + 8 * to, total);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      bulk_load(smem_u32(buf + (to * N + i) * slot_bytes), reinterpret_cast<const uint8_t*>((uintptr_t)src[i] & ~(uintptr_t)15),
+                bytes[i], bar + 8 * to);
+  }
+  __device__ __forceinline__ bool wait() const {
+    return __all_sync(0xffffffffu, mbar_wait_short(bar + 8 * slot, phase, abort_word, DEV_TIMEOUT_PRODUCER, kWaitNs));
+  }
+  // Row i of the current slot, whose source is src.
+  __device__ __forceinline__ const T* row(int i, const T* src) const {
+    return reinterpret_cast<const T*>(buf + (slot * N + i) * slot_bytes + ((uint32_t)(uintptr_t)src & 15u));
+  }
+  __device__ __forceinline__ void next() {
+    if (++slot == slots) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// Barriers of a block's slots (at most kBars in all).
+constexpr int kBars = 128;
+__device__ __forceinline__ void init_bars(uint64_t* bars, uint32_t* abort, int n) {
+  for (int i = threadIdx.x; i < n; i += blockDim.x) mbar_init(smem_u32(bars + i), 1);
+  if (threadIdx.x == 0) *abort = 0;
+  fence_mbar_init();
   __syncthreads();
-  x = warp_sum(lane < nw ? red[lane] : 0.f);
-  __syncthreads();
-  return x;
+}
+__device__ __forceinline__ void report(const uint32_t* abort) {
+  const int code = *reinterpret_cast<const volatile int*>(abort);
+  if (code == 0) return;
+  if ((threadIdx.x & 31) == 0) atomicExch(&g_error, code);
+  settle();
 }
 
-// Two sums with one pair of barriers.
-template <bool WARP>
-__device__ __forceinline__ float2 row_sum2(float a, float b, float2* red) {
-  a = warp_sum(a);
-  b = warp_sum(b);
-  if (WARP) return make_float2(a, b);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
-  if (lane == 0) red[warp] = make_float2(a, b);
-  __syncthreads();
-  const float2 v = lane < nw ? red[lane] : make_float2(0.f, 0.f);
-  a = warp_sum(v.x);
-  b = warp_sum(v.y);
-  __syncthreads();
-  return make_float2(a, b);
+// The vector's registers as values the compiler knows nothing about.
+template <typename T, int VEC>
+__device__ __forceinline__ void opaque(Vec<T, VEC>& v) {
+  if constexpr (VEC * sizeof(T) >= 4) {
+#pragma unroll
+    for (int i = 0; i < (int)(VEC * sizeof(T) / 4); ++i) asm volatile("" : "+r"(reinterpret_cast<uint32_t*>(&v)[i]));
+  }
 }
 
-template <typename T, typename W, int VEC, bool WARP, int MAXT>
-__global__ void __launch_bounds__(MAXT) norm_fwd_kernel(const NormArgs p) {
-  constexpr int NV = kElems / VEC;
-  __shared__ float red[32];
-  const int tpr = WARP ? 32 : blockDim.x;                       // threads of a row
-  const int t = WARP ? (threadIdx.x & 31) : threadIdx.x;
-  const int64_t row = WARP ? (int64_t)blockIdx.x * kWarpRows + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
-  if (WARP && row >= p.total) return;
-  const int64_t s = row / p.rows, i = row - s * p.rows;
-  const T* x = static_cast<const T*>(p.x) + s * p.x_batch + i * p.x_row;
-  float v[NV][VEC];
-  float sum = 0.f;
+template <typename T, typename W, int VEC, int NV, bool MULTI>
+__global__ void __launch_bounds__(512) norm_fwd_kernel(const NormArgs p) {
+  __shared__ float2 red[64];
+  __shared__ uint64_t bars[kBars];
+  __shared__ uint32_t abort_word;
+  extern __shared__ __align__(16) uint8_t smem[];
+  init_bars(bars, &abort_word, p.at_once * p.slots);
+  Row<MULTI> me(p, red);
+  Ring<T, 1> ring(p, me.group, bars, smem, &abort_word);
+  const int64_t first = (int64_t)blockIdx.x * p.at_once + me.group, step = (int64_t)gridDim.x * p.at_once;
+  auto source = [&](int64_t row) {
+    const uint32_t s = p.div_rows.div((uint32_t)row), i = (uint32_t)row - s * p.rows;
+    return static_cast<const T*>(p.x) + s * p.x_batch + i * p.x_row;
+  };
+  if (me.t == 0)
+    for (int k = 0; k < p.slots && first + k * step < p.total; ++k) {
+      const T* src[1] = {source(first + k * step)};
+      ring.issue(k, src);
+    }
+  for (int64_t row = first; row < p.total; row += step, ring.next()) {
+    const uint32_t s = p.div_rows.div((uint32_t)row), i = (uint32_t)row - s * p.rows;
+    const T* x = ring.row(0, static_cast<const T*>(p.x) + s * p.x_batch + i * p.x_row);
+    const bool ok = ring.wait();       // (after one that ran out the rows' barriers are still kept)
+    Vec<T, VEC> v[NV];
+    float sum = 0.f;
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int c = (t + k * tpr) * VEC;
-    if (c < p.C) {
-      load_f32<T, VEC>(x + c, v[k]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) v[k][e] = 0.f;
+    for (int k = 0; k < NV; ++k) {
+      const int c = (me.t + k * me.threads) * VEC;
+      v[k] = c < p.C ? *reinterpret_cast<const Vec<T, VEC>*>(x + c) : Vec<T, VEC>{};
     }
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) sum += v[k][e];
-  }
-  const float mean = row_sum<WARP>(sum, red) * p.inv_c;
-  float sq = 0.f;
+    for (int k = 0; k < NV; ++k)
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int c = (t + k * tpr) * VEC;
+      for (int e = 0; e < VEC; ++e) sum += to_f32(v[k].v[e]);
+    const float mean = me.sum(make_float2(sum, 0.f), p.warps).x * p.inv_c;
+    if (me.t == 0 && ok && row + p.slots * step < p.total) {     // every thread of the row has read its slot
+      const T* src[1] = {source(row + p.slots * step)};
+      ring.issue(ring.slot, src);
+    }
+    float sq = 0.f;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      v[k][e] -= mean;
-      if (c < p.C) sq += v[k][e] * v[k][e];
+    for (int k = 0; k < NV; ++k) {
+      opaque(v[k]);                    // convert again instead of keeping fp32 copies
+      if ((me.t + k * me.threads) * VEC >= p.C) continue;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float d = to_f32(v[k].v[e]) - mean;
+        sq += d * d;
+      }
+    }
+    const float rstd = 1.0f / sqrtf(me.sum(make_float2(sq, 0.f), p.warps).x * p.inv_c + p.eps);
+    if (!ok) continue;
+    T* y = static_cast<T*>(p.y) + s * p.y_batch + i * p.y_row;
+    const W* w = p.w ? static_cast<const W*>(p.w) + s * p.w_batch : nullptr;
+    const W* b = p.b ? static_cast<const W*>(p.b) + s * p.w_batch : nullptr;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      opaque(v[k]);
+      const int c = (me.t + k * me.threads) * VEC;
+      if (c >= p.C) continue;
+      float wv[VEC], bv[VEC];
+      if (w) load_f32<W, VEC>(w + c, wv);
+      if (b) load_f32<W, VEC>(b + c, bv);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        v[k].v[e] = from_f32<T>((to_f32(v[k].v[e]) - mean) * rstd * (w ? wv[e] + p.plus : 1.0f) + (b ? bv[e] : 0.0f));
+      *reinterpret_cast<Vec<T, VEC>*>(y + c) = v[k];
+    }
+    if (me.t == 0) {
+      if (p.mean) p.mean[row] = mean;
+      if (p.rstd) p.rstd[row] = rstd;
     }
   }
-  const float rstd = 1.0f / sqrtf(row_sum<WARP>(sq, red) * p.inv_c + p.eps);
-  T* y = static_cast<T*>(p.y) + s * p.y_batch + i * p.y_row;
-  const W* w = p.w ? static_cast<const W*>(p.w) + s * p.w_batch : nullptr;
-  const W* b = p.b ? static_cast<const W*>(p.b) + s * p.w_batch : nullptr;
-#pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int c = (t + k * tpr) * VEC;
-    if (c >= p.C) continue;
-    float wv[VEC], bv[VEC];
-    if (w) load_f32<W, VEC>(w + c, wv);
-    if (b) load_f32<W, VEC>(b + c, bv);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e)
-      v[k][e] = v[k][e] * rstd * (w ? wv[e] + p.plus : 1.0f) + (b ? bv[e] : 0.0f);
-    store_f32<T, VEC>(y + c, v[k]);
-  }
-  if (t == 0) {
-    if (p.mean) p.mean[row] = mean;
-    if (p.rstd) p.rstd[row] = rstd;
-  }
+  report(&abort_word);
 }
 
-// One block walks the rows [r0, r1) of run blockIdx.x; with WARP its warps take them in turn.
-template <typename T, typename W, int VEC, bool WARP, int MAXT>
-__global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormArgs p) {
-  constexpr int NV = kElems / VEC;
-  __shared__ float2 red[32];
-  const int tpr = WARP ? 32 : blockDim.x;
-  const int t = WARP ? (threadIdx.x & 31) : threadIdx.x;
-  const int warp = WARP ? threadIdx.x >> 5 : 0, step = WARP ? kWarpRows : 1;
+// One block walks the rows [r0, r1) of run blockIdx.x, its row groups in turn.
+template <typename T, typename W, int VEC, int NV, bool MULTI>
+__global__ void __launch_bounds__(512) norm_bwd_kernel(const NormArgs p) {
+  __shared__ float2 red[64];
+  __shared__ uint64_t bars[kBars];
+  __shared__ uint32_t abort_word;
+  extern __shared__ __align__(16) uint8_t smem[];
+  float* acc = reinterpret_cast<float*>(smem);       // [2][C] at the end, when a block holds several rows
+  init_bars(bars, &abort_word, p.at_once * p.slots);
+  Row<MULTI> me(p, red);
+  Ring<T, 2> ring(p, me.group, bars, smem, &abort_word);
   const int64_t group = blockIdx.x / p.runs_per_group;
   const int64_t run = blockIdx.x - group * p.runs_per_group;
   const int64_t r0 = group * p.group_rows + p.group_rows * run / p.runs_per_group;
@@ -159,144 +256,209 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormArgs p) {
   for (int k = 0; k < NV; ++k)
 #pragma unroll
     for (int e = 0; e < VEC; ++e) dw[k][e] = db[k][e] = 0.f;
-  for (int64_t row = r0 + warp; row < r1; row += step) {
-    const int64_t s = row / p.rows, i = row - s * p.rows;
-    const T* x = static_cast<const T*>(p.x) + s * p.x_batch + i * p.x_row;
-    const T* dy = static_cast<const T*>(p.dy) + s * p.dy_batch + i * p.dy_row;
+  auto issue = [&](int slot, int64_t row) {
+    const uint32_t s = p.div_rows.div((uint32_t)row), i = (uint32_t)row - s * p.rows;
+    const T* src[2] = {static_cast<const T*>(p.x) + s * p.x_batch + i * p.x_row,
+                       static_cast<const T*>(p.dy) + s * p.dy_batch + i * p.dy_row};
+    ring.issue(slot, src);
+  };
+  if (me.t == 0)
+    for (int k = 0; k < p.slots && r0 + me.group + k * p.at_once < r1; ++k) issue(k, r0 + me.group + k * p.at_once);
+  for (int64_t row = r0 + me.group; row < r1; row += p.at_once, ring.next()) {
+    const uint32_t s = p.div_rows.div((uint32_t)row), i = (uint32_t)row - s * p.rows;
+    const T* x = ring.row(0, static_cast<const T*>(p.x) + s * p.x_batch + i * p.x_row);
+    const T* dy = ring.row(1, static_cast<const T*>(p.dy) + s * p.dy_batch + i * p.dy_row);
+    const float mean = __ldg(p.mean + row), rstd = __ldg(p.rstd + row);
+    const bool ok = ring.wait();       // (after one that ran out the rows' barriers are still kept)
     const W* w = p.w ? static_cast<const W*>(p.w) + s * p.w_batch : nullptr;
-    const float mean = p.mean[row], rstd = p.rstd[row];
-    float xh[NV][VEC], g[NV][VEC];
+    Vec<T, VEC> xv[NV], gv[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int c = (me.t + k * me.threads) * VEC;
+      const bool in = c < p.C;
+      xv[k] = in ? *reinterpret_cast<const Vec<T, VEC>*>(x + c) : Vec<T, VEC>{};
+      gv[k] = in ? *reinterpret_cast<const Vec<T, VEC>*>(dy + c) : Vec<T, VEC>{};
+    }
     float a = 0.f, b = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int c = (t + k * tpr) * VEC;
-      if (c < p.C) {
-        load_f32<T, VEC>(x + c, xh[k]);
-        load_f32<T, VEC>(dy + c, g[k]);
-        float wv[VEC];
-        if (w) load_f32<W, VEC>(w + c, wv);
+      const int c = (me.t + k * me.threads) * VEC;
+      if (c >= p.C) continue;
+      float wv[VEC];
+      if (w) load_f32<W, VEC>(w + c, wv);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          xh[k][e] = (xh[k][e] - mean) * rstd;
-          dw[k][e] += g[k][e] * xh[k][e];
-          db[k][e] += g[k][e];
-          if (w) g[k][e] *= wv[e] + p.plus;
-          a += g[k][e];
-          b += g[k][e] * xh[k][e];
-        }
+      for (int e = 0; e < VEC; ++e) {
+        const float xh = (to_f32(xv[k].v[e]) - mean) * rstd;
+        float g = to_f32(gv[k].v[e]);
+        dw[k][e] += g * xh;
+        db[k][e] += g;
+        if (w) g *= wv[e] + p.plus;
+        a += g;
+        b += g * xh;
       }
     }
-    const float2 ab = row_sum2<WARP>(a, b, red);
+    const float2 ab = me.sum(make_float2(a, b), p.warps);
+    if (me.t == 0 && ok && row + (int64_t)p.slots * p.at_once < r1) issue(ring.slot, row + (int64_t)p.slots * p.at_once);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {     // convert again below instead of keeping fp32 copies
+      opaque(xv[k]);
+      opaque(gv[k]);
+    }
+    const float am = ab.x * p.inv_c, bm = ab.y * p.inv_c;
+    if (!ok) continue;
     T* dx = static_cast<T*>(p.y) + s * p.y_batch + i * p.y_row;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int c = (t + k * tpr) * VEC;
+      const int c = (me.t + k * me.threads) * VEC;
       if (c >= p.C) continue;
+      float wv[VEC];
+      if (w) load_f32<W, VEC>(w + c, wv);           // (again: cheaper than keeping g in fp32)
 #pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        g[k][e] = rstd * (g[k][e] - ab.x * p.inv_c - xh[k][e] * (ab.y * p.inv_c));
-      store_f32<T, VEC>(dx + c, g[k]);
+      for (int e = 0; e < VEC; ++e) {
+        const float xh = (to_f32(xv[k].v[e]) - mean) * rstd;
+        const float g = to_f32(gv[k].v[e]) * (w ? wv[e] + p.plus : 1.0f);
+        gv[k].v[e] = from_f32<T>(rstd * (g - am - xh * bm));
+      }
+      *reinterpret_cast<Vec<T, VEC>*>(dx + c) = gv[k];
     }
   }
+  report(&abort_word);
   if (!p.part) return;
   float* out = p.part + (int64_t)blockIdx.x * 2 * p.C;
-  if constexpr (WARP) {
-    // the block's warps hold sums of the same columns: add them in warp order
-    __shared__ float acc[2][kWarpCols];
-    for (int q = 0; q < kWarpRows; ++q) {
-      if (warp == q) {
+  if (p.at_once > 1) __syncthreads();  // the slots' memory is used again
+  // the block's row groups hold sums of the same columns: add them in order
+  for (int q = 0; q < p.at_once; ++q) {
+    if (me.group == q) {
+      float* to = p.at_once > 1 && q + 1 < p.at_once ? acc : out;
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
+      for (int k = 0; k < NV; ++k)
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const int c = (t + k * 32) * VEC + e;
-            acc[0][c] = dw[k][e] + (q ? acc[0][c] : 0.f);
-            acc[1][c] = db[k][e] + (q ? acc[1][c] : 0.f);
-          }
-      }
-      __syncthreads();
-    }
-    for (int c = threadIdx.x; c < p.C; c += blockDim.x) {
-      out[c] = acc[0][c];
-      out[p.C + c] = acc[1][c];
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int c = (t + k * tpr) * VEC;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        if (c + e < p.C) {
-          out[c + e] = dw[k][e];
-          out[p.C + c + e] = db[k][e];
+        for (int e = 0; e < VEC; ++e) {
+          const int c = (me.t + k * me.threads) * VEC + e;
+          if (c >= p.C) continue;
+          to[c] = dw[k][e] + (q ? acc[c] : 0.f);
+          to[p.C + c] = db[k][e] + (q ? acc[p.C + c] : 0.f);
         }
     }
+    if (p.at_once > 1) __syncthreads();
   }
 }
 
-// Adds the runs of a group: block (32 columns, 8 lanes of runs), grid (columns / 32, groups, 2).
+// Adds the runs of a group: block (32 columns, 32 lanes of runs), grid (columns / 32, groups, 2).
 template <typename O>
-__global__ void __launch_bounds__(256) norm_reduce_kernel(const float* part, int C, int runs, O* dw, O* db) {
+__global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* part, int C, int runs, O* dw, O* db) {
   O* out = blockIdx.z ? db : dw;
   if (!out) return;
-  __shared__ float acc[8][33];
+  __shared__ float acc[32][33];
   const int c = blockIdx.x * 32 + threadIdx.x;
   const int64_t g = blockIdx.y;
   float s = 0.f;
   if (c < C)
-    for (int r = threadIdx.y; r < runs; r += 8) s += part[((g * runs + r) * 2 + blockIdx.z) * C + c];
+    for (int r = threadIdx.y; r < runs; r += 32) s += part[((g * runs + r) * 2 + blockIdx.z) * C + c];
   acc[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
-  if (threadIdx.y == 0 && c < C) {
-#pragma unroll
-    for (int q = 1; q < 8; ++q) s += acc[q][threadIdx.x];
-    out[g * C + c] = from_f32<O>(s);
-  }
+  // warp y adds column y's 32 lanes, in the order of a fixed tree
+  s = warp_sum(acc[threadIdx.x][threadIdx.y]);
+  const int col = blockIdx.x * 32 + threadIdx.y;
+  if (threadIdx.x == 0 && col < C) out[g * C + col] = from_f32<O>(s);
 }
 
-// Threads of a row's block: one warp up to kWarpCols columns, else just enough warps.
-int row_threads(int C) { return std::max(32, (C + kWarpCols - 1) / kWarpCols * 32); }
+// How a row is spread: its warps and its vectors per lane, of `most` at most.
+struct Spread {
+  int warps, nv;
+};
+Spread spread(int C, int vec, int most) {
+  const int pieces = (C + vec - 1) / vec;                  // vectors of a row
+  const int warps = (pieces + 32 * most - 1) / (32 * most);
+  return {warps, (pieces + 32 * warps - 1) / (32 * warps)};
+}
+// Vectors per lane at most: 64 elements of 16 bits, 32 of 32 bits; the backward pass, with two sums
+// beside each element, 24 and 16; one by one (unaligned rows) 16.  The widest rows take 32 elements,
+// so that 16 warps hold them.
+int most_vectors(bool bwd, int vec, int C) {
+  if (vec == 8) return bwd ? (C <= 12288 ? 3 : 4) : 8;
+  if (vec == 4) return bwd && C <= 8192 ? 4 : 8;
+  return C <= 8192 ? 16 : 32;
+}
+constexpr int kSmem = 200 * 1024;      // dynamic shared memory of a block at most
 
-// Runs of a group in the backward pass: about 512 threads per multiprocessor (its accumulators
-// take about 128 registers), no more runs than rows.
-int runs_of(int64_t group_rows, int64_t groups, int C, int sms) {
-  const int block = C <= kWarpCols ? 32 * kWarpRows : row_threads(C);
-  const int64_t want = std::max<int64_t>(1, (int64_t)sms * std::max(1, 512 / block) / groups);
-  const int64_t most = C <= kWarpCols ? (group_rows + kWarpRows - 1) / kWarpRows : group_rows;
-  return (int)std::max<int64_t>(1, std::min(want, most));
+// Rows of a block at a time (16 warps, one block per multiprocessor; named barriers give 15 groups of
+// warps), and the rows in flight behind each: as many as fit, 8 at most.  The backward pass's groups
+// leave their sums in the same memory.
+void plan_block(NormArgs& a, bool bwd, int elem, int64_t rows_per_block) {
+  const int tensors = bwd ? 2 : 1;
+  a.slot_bytes = (a.C * elem + 31) & ~15;                  // a row that starts anywhere
+  a.at_once = a.warps > 1 ? std::min(15, 16 / a.warps) : 16;
+  a.at_once = (int)std::max<int64_t>(1, std::min<int64_t>(a.at_once, rows_per_block));
+  a.at_once = std::min(a.at_once, std::max(1, kSmem / (tensors * a.slot_bytes)));
+  if (bwd && 2 * a.C * (int)sizeof(float) > kSmem) a.at_once = 1;
+  a.slots = std::max(1, std::min(8, kSmem / (a.at_once * tensors * a.slot_bytes)));
+}
+int smem_bytes(const NormArgs& a, bool bwd) {
+  const int ring = a.at_once * a.slots * (bwd ? 2 : 1) * a.slot_bytes;
+  return std::max(ring, bwd && a.at_once > 1 ? 2 * a.C * (int)sizeof(float) : 0);
 }
 
-template <typename T, typename W, int VEC>
-cudaError_t launch_vec(bool bwd, const NormArgs& a, int blocks, cudaStream_t st) {
-  const int tpr = row_threads(a.C);
-  if (a.C <= kWarpCols) {
-    if (bwd) norm_bwd_kernel<T, W, VEC, true, 256><<<blocks, 32 * kWarpRows, 0, st>>>(a);
-    else norm_fwd_kernel<T, W, VEC, true, 256><<<blocks, 32 * kWarpRows, 0, st>>>(a);
-  } else if (tpr <= 512) {
-    if (bwd) norm_bwd_kernel<T, W, VEC, false, 512><<<blocks, tpr, 0, st>>>(a);
-    else norm_fwd_kernel<T, W, VEC, false, 512><<<blocks, tpr, 0, st>>>(a);
-  } else {
-    if (bwd) norm_bwd_kernel<T, W, VEC, false, 1024><<<blocks, tpr, 0, st>>>(a);
-    else norm_fwd_kernel<T, W, VEC, false, 1024><<<blocks, tpr, 0, st>>>(a);
+// Runs of a group in the backward pass: one block per multiprocessor, no more than rows.
+int runs_of(int64_t group_rows, int64_t groups, int sms) {
+  return (int)std::max<int64_t>(1, std::min(std::max<int64_t>(1, sms / groups), group_rows));
+}
+
+template <typename K>
+cudaError_t launch_one(K kernel, int blocks, int threads, int smem, const NormArgs& a, cudaStream_t st) {
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
   }
+  kernel<<<blocks, threads, smem, st>>>(a);
   return cudaGetLastError();
 }
 
-template <typename T, typename W>
-cudaError_t launch_norm(bool bwd, bool vec, const NormArgs& a, int blocks, cudaStream_t st) {
-  return vec ? launch_vec<T, W, (int)(16 / sizeof(T))>(bwd, a, blocks, st)
-             : launch_vec<T, W, 1>(bwd, a, blocks, st);
+template <typename T, typename W, int VEC, int NV>
+cudaError_t launch_nv(bool bwd, const NormArgs& a, int blocks, cudaStream_t st) {
+  const int threads = 32 * a.warps * a.at_once, smem = smem_bytes(a, bwd);
+  if (!bwd)
+    return a.warps > 1 ? launch_one(norm_fwd_kernel<T, W, VEC, NV, true>, blocks, threads, smem, a, st)
+                       : launch_one(norm_fwd_kernel<T, W, VEC, NV, false>, blocks, threads, smem, a, st);
+  if constexpr (VEC * NV <= 32)                            // (no wider: see most_vectors)
+    return a.warps > 1 ? launch_one(norm_bwd_kernel<T, W, VEC, NV, true>, blocks, threads, smem, a, st)
+                       : launch_one(norm_bwd_kernel<T, W, VEC, NV, false>, blocks, threads, smem, a, st);
+  return cudaErrorInvalidValue;
 }
 
-cudaError_t dispatch(bool bwd, int dtype, int wdtype, bool vec, const NormArgs& a, int blocks, cudaStream_t st) {
+template <typename T, typename W, int VEC>
+cudaError_t launch_vec(bool bwd, const NormArgs& a, int nv, int blocks, cudaStream_t st) {
+  if constexpr (VEC == 1) {
+    return nv <= 4 ? launch_nv<T, W, 1, 4>(bwd, a, blocks, st) : nv <= 8  ? launch_nv<T, W, 1, 8>(bwd, a, blocks, st)
+           : nv <= 16 ? launch_nv<T, W, 1, 16>(bwd, a, blocks, st)
+                      : launch_nv<T, W, 1, 32>(bwd, a, blocks, st);
+  } else {
+    switch (nv) {
+      case 1: return launch_nv<T, W, VEC, 1>(bwd, a, blocks, st);
+      case 2: return launch_nv<T, W, VEC, 2>(bwd, a, blocks, st);
+      case 3: return launch_nv<T, W, VEC, 3>(bwd, a, blocks, st);
+      default: break;
+    }
+    if (nv <= 4) return launch_nv<T, W, VEC, 4>(bwd, a, blocks, st);
+    if (nv <= 6) return launch_nv<T, W, VEC, 6>(bwd, a, blocks, st);
+    return launch_nv<T, W, VEC, 8>(bwd, a, blocks, st);
+  }
+}
+
+template <typename T, typename W>
+cudaError_t launch_norm(bool bwd, int vec, const NormArgs& a, int nv, int blocks, cudaStream_t st) {
+  return vec > 1 ? launch_vec<T, W, (int)(16 / sizeof(T))>(bwd, a, nv, blocks, st) : launch_vec<T, W, 1>(bwd, a, nv, blocks, st);
+}
+
+cudaError_t dispatch(bool bwd, int dtype, int wdtype, int vec, const NormArgs& a, int nv, int blocks, cudaStream_t st) {
   const bool wf = wdtype == ULTRAGEN_F32;
   if (dtype == ULTRAGEN_BF16)
-    return wf ? launch_norm<__nv_bfloat16, float>(bwd, vec, a, blocks, st)
-              : launch_norm<__nv_bfloat16, __nv_bfloat16>(bwd, vec, a, blocks, st);
+    return wf ? launch_norm<__nv_bfloat16, float>(bwd, vec, a, nv, blocks, st)
+              : launch_norm<__nv_bfloat16, __nv_bfloat16>(bwd, vec, a, nv, blocks, st);
   if (dtype == ULTRAGEN_F16)
-    return wf ? launch_norm<__half, float>(bwd, vec, a, blocks, st)
-              : launch_norm<__half, __half>(bwd, vec, a, blocks, st);
-  return launch_norm<float, float>(bwd, vec, a, blocks, st);
+    return wf ? launch_norm<__half, float>(bwd, vec, a, nv, blocks, st)
+              : launch_norm<__half, __half>(bwd, vec, a, nv, blocks, st);
+  return launch_norm<float, float>(bwd, vec, a, nv, blocks, st);
 }
 
 int elem_size(int dtype) { return dtype == ULTRAGEN_F32 ? 4 : 2; }
@@ -321,6 +483,7 @@ NormArgs args_of(const ultragen_norm_t* n) {
   NormArgs a = {};
   a.total = (int64_t)n->batch * n->rows;
   a.rows = n->rows;
+  a.div_rows = FastDiv((uint32_t)std::max(1, n->rows));
   a.C = n->cols;
   a.w_batch = n->per_sample ? n->cols : 0;
   a.plus = n->plus_one ? 1.0f : 0.0f;
@@ -337,19 +500,24 @@ NormArgs args_of(const ultragen_norm_t* n) {
 }
 
 // 16-byte vectors need every row, and every sample's weight, to start on a 16-byte boundary (a
-// weight wider than the rows then does too, its vectors being a multiple of theirs).
-bool vectorised(const ultragen_norm_t* n, const void* x, const void* dy, const void* y, const void* w,
+// weight wider than the rows then does too, its vectors being a multiple of theirs).  Returns the
+// elements of a vector, 1 without.
+int vectorised(const ultragen_norm_t* n, const void* x, const void* dy, const void* y, const void* w,
                 const void* b) {
   const int vec = 16 / elem_size(n->dtype);
   const int64_t wb = n->per_sample ? n->cols : 0;
-  return n->cols % vec == 0 && rows16(x, n->x_row, n->x_batch, vec, n->dtype) &&
+  const bool ok = n->cols % vec == 0 && rows16(x, n->x_row, n->x_batch, vec, n->dtype) &&
          rows16(dy, n->dy_row, n->dy_batch, vec, n->dtype) && rows16(y, n->y_row, n->y_batch, vec, n->dtype) &&
          rows16(w, wb, wb, vec, n->wdtype) && rows16(b, wb, wb, vec, n->wdtype);
+  return ok ? vec : 1;
 }
 
 int status_of(cudaError_t e) { return e == cudaSuccess ? ULTRAGEN_OK : ULTRAGEN_ERR_CUDA; }
 
 }  // namespace
+
+cudaError_t norm_status(int* code, cudaStream_t s) { return read_clear_error(&g_error, code, s); }
+
 }  // namespace ug
 
 using namespace ug;
@@ -372,8 +540,12 @@ int ultragen_layer_norm(const ultragen_norm_t* n, const void* x, const void* wei
   a.y = y;
   a.mean = mean;
   a.rstd = rstd;
-  const int blocks = (int)(n->cols <= kWarpCols ? (a.total + kWarpRows - 1) / kWarpRows : a.total);
-  return status_of(dispatch(false, n->dtype, n->wdtype, vectorised(n, x, nullptr, y, weight, bias), a, blocks,
+  const int vec = vectorised(n, x, nullptr, y, weight, bias);
+  const Spread sp = spread(n->cols, vec, most_vectors(false, vec, n->cols));
+  a.warps = sp.warps;
+  plan_block(a, false, elem_size(n->dtype), (a.total + sm_count() - 1) / sm_count());
+  const int64_t blocks = std::min<int64_t>((a.total + a.at_once - 1) / a.at_once, sm_count());
+  return status_of(dispatch(false, n->dtype, n->wdtype, vec, a, sp.nv, (int)blocks,
                             reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -383,7 +555,7 @@ int ultragen_layer_norm_backward_workspace(const ultragen_norm_t* n, size_t* byt
   if (!bytes) return ULTRAGEN_ERR_INVALID_ARG;
   const NormArgs a = args_of(n);
   const int64_t groups = n->per_sample ? n->batch : 1;
-  *bytes = a.total == 0 ? 0 : (size_t)groups * runs_of(a.group_rows, groups, n->cols, sm_count()) * 2 * n->cols * sizeof(float);
+  *bytes = a.total == 0 ? 0 : (size_t)groups * runs_of(a.group_rows, groups, sm_count()) * 2 * n->cols * sizeof(float);
   return ULTRAGEN_OK;
 }
 
@@ -408,7 +580,11 @@ int ultragen_layer_norm_backward(const ultragen_norm_t* n, const void* dy, const
   }
   if (!dy || !x || !mean || !rstd || !dx) return ULTRAGEN_ERR_INVALID_ARG;
   if ((st = current_device(&dev)) != ULTRAGEN_OK) return st;
-  a.runs_per_group = runs_of(a.group_rows, groups, n->cols, sm_count());
+  const int vec = vectorised(n, x, dy, dx, weight, nullptr);
+  const Spread sp = spread(n->cols, vec, most_vectors(true, vec, n->cols));
+  a.warps = sp.warps;
+  a.runs_per_group = runs_of(a.group_rows, groups, sm_count());
+  plan_block(a, true, elem_size(n->dtype), (a.group_rows + a.runs_per_group - 1) / a.runs_per_group);
   if (dweight || dbias) {
     const size_t need = (size_t)groups * a.runs_per_group * 2 * n->cols * sizeof(float);
     if (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 15u)) return ULTRAGEN_ERR_INVALID_ARG;
@@ -421,10 +597,9 @@ int ultragen_layer_norm_backward(const ultragen_norm_t* n, const void* dy, const
   a.mean = const_cast<float*>(mean);
   a.rstd = const_cast<float*>(rstd);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  st = status_of(dispatch(true, n->dtype, n->wdtype, vectorised(n, x, dy, dx, weight, nullptr), a,
-                          (int)(groups * a.runs_per_group), s));
+  st = status_of(dispatch(true, n->dtype, n->wdtype, vec, a, sp.nv, (int)(groups * a.runs_per_group), s));
   if (st != ULTRAGEN_OK || !a.part) return st;
-  const dim3 grid((n->cols + 31) / 32, (unsigned)groups, 2), block(32, 8);
+  const dim3 grid((n->cols + 31) / 32, (unsigned)groups, 2), block(32, 32);
   if (grad_dtype == ULTRAGEN_F32)
     norm_reduce_kernel<float><<<grid, block, 0, s>>>(a.part, n->cols, a.runs_per_group, (float*)dweight, (float*)dbias);
   else if (grad_dtype == ULTRAGEN_BF16)
