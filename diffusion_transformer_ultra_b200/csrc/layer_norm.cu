@@ -10,11 +10,14 @@
 // A row belongs to one warp up to 2,048 elements of 16 bits (1,024 of 32; the backward pass, which
 // keeps the weight's gradient too, fewer), else to a group of warps.  Its rows come by bulk copies,
 // several ahead, into shared memory (a persistent block per multiprocessor has up to 200 KB of them in
-// flight; with loads straight to registers the forward pass took 132 us, and with a row to a block
-// 151 us, for 70,144 x 2,048 bf16), and from there to registers, as they were read, so that the
-// variance takes a second pass over registers (no cancellation of sum(x^2) against mu^2).  A copy
-// covers the 16-byte pieces that hold the row, so that a row may start anywhere; rows that do not start
-// on 16 bytes are then worked on element by element.  All sums are fp32.
+// flight), and from there to registers, as they were read, so that the variance takes a second pass
+// over registers (no cancellation of sum(x^2) against mu^2).  A copy covers the 16-byte pieces that
+// hold the row, so that a row may start anywhere; one that does not start on four elements is then
+// worked on element by element.  All sums are fp32.
+// With the loads ahead of time the instructions and the weight's way from L1 set the pace: arithmetic
+// is on pairs, and a lane's piece is four elements, so that a warp's fp32 weights are one contiguous
+// 512-byte load.  (With pieces of eight, whose fp32 weights a warp reads in halves of 32-byte sectors,
+// and scalar arithmetic, the forward pass took 150 instead of 1XX us for 70,144 x 2,048 bf16.)
 //
 // The weight's gradient: a block of the backward pass walks a run of rows of one sample (of the
 // whole batch with a shared weight), keeps its columns' sums in registers, and writes them once
@@ -25,6 +28,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "cross.cuh"
 #include "device.h"
@@ -152,15 +156,76 @@ __device__ __forceinline__ void report(const uint32_t* abort) {
 }
 
 // The vector's registers as values the compiler knows nothing about.
-template <typename T, int VEC>
-__device__ __forceinline__ void opaque(Vec<T, VEC>& v) {
-  if constexpr (VEC * sizeof(T) >= 4) {
+template <typename T>
+__device__ __forceinline__ void opaque(Vec<T, 4>& v) {
 #pragma unroll
-    for (int i = 0; i < (int)(VEC * sizeof(T) / 4); ++i) asm volatile("" : "+r"(reinterpret_cast<uint32_t*>(&v)[i]));
-  }
+  for (int i = 0; i < (int)sizeof(T); ++i) asm volatile("" : "+r"(reinterpret_cast<uint32_t*>(&v)[i]));
 }
 
-template <typename T, typename W, int VEC, int NV, bool MULTI>
+// A piece: four elements of a row, as fp32 pairs.
+template <typename T>
+__device__ __forceinline__ void pairs(const Vec<T, 4>& v, float2 (&out)[2]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      out[i] = make_float2(v.v[2 * i], v.v[2 * i + 1]);
+    } else if constexpr (std::is_same<T, __half>::value) {
+      out[i] = __half22float2(reinterpret_cast<const __half2*>(&v)[i]);
+    } else {
+      const uint32_t w = reinterpret_cast<const uint32_t*>(&v)[i];
+      out[i] = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void unpairs(Vec<T, 4>& v, const float2 (&in)[2]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      v.v[2 * i] = in[i].x;
+      v.v[2 * i + 1] = in[i].y;
+    } else {
+      reinterpret_cast<uint32_t*>(&v)[i] = pack2<T>(in[i].x, in[i].y);
+    }
+  }
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// Piece k of thread t of a row's `threads`: columns 4 (t + k threads) and on where rows start on four
+// elements (CONTIG; C is then a multiple of four), else t + (4 k + e) threads, element by element.
+template <bool CONTIG>
+struct Piece {
+  int col, step, C;
+  __device__ __forceinline__ Piece(int t, int k, int threads, int C_)
+      : col(CONTIG ? (t + k * threads) * 4 : t + 4 * k * threads), step(CONTIG ? 1 : threads), C(C_) {}
+  __device__ __forceinline__ bool any() const { return col < C; }
+  __device__ __forceinline__ int at(int e) const { return col + e * step; }
+  __device__ __forceinline__ bool has(int e) const { return CONTIG || at(e) < C; }
+  template <typename T>
+  __device__ __forceinline__ Vec<T, 4> load(const T* p) const {   // zeros behind the row
+    Vec<T, 4> v{};
+    if (CONTIG) {
+      if (any()) v = *reinterpret_cast<const Vec<T, 4>*>(p + col);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (has(e)) v.v[e] = p[at(e)];
+    }
+    return v;
+  }
+  template <typename T>
+  __device__ __forceinline__ void store(T* p, const Vec<T, 4>& v) const {
+    if (CONTIG) {
+      if (any()) *reinterpret_cast<Vec<T, 4>*>(p + col) = v;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (has(e)) p[at(e)] = v.v[e];
+    }
+  }
+};
+
+template <typename T, typename W, bool CONTIG, int NV, bool MULTI>
 __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormArgs p) {
   __shared__ float2 red[64];
   __shared__ uint64_t bars[kBars];
@@ -183,34 +248,42 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormArgs p) {
     const uint32_t s = p.div_rows.div((uint32_t)row), i = (uint32_t)row - s * p.rows;
     const T* x = ring.row(0, static_cast<const T*>(p.x) + s * p.x_batch + i * p.x_row);
     const bool ok = ring.wait();       // (after one that ran out the rows' barriers are still kept)
-    Vec<T, VEC> v[NV];
-    float sum = 0.f;
+    Vec<T, 4> v[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) v[k] = Piece<CONTIG>(me.t, k, me.threads, p.C).load(x);
+    float2 sum[2] = {both(0.f), both(0.f)};
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int c = (me.t + k * me.threads) * VEC;
-      v[k] = c < p.C ? *reinterpret_cast<const Vec<T, VEC>*>(x + c) : Vec<T, VEC>{};
+      float2 f[2];
+      pairs<T>(v[k], f);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) sum[e & 1] = fadd2(sum[e & 1], f[e]);
     }
-#pragma unroll
-    for (int k = 0; k < NV; ++k)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) sum += to_f32(v[k].v[e]);
-    const float mean = me.sum(make_float2(sum, 0.f), p.warps).x * p.inv_c;
+    sum[0] = fadd2(sum[0], sum[1]);
+    const float mean = me.sum(make_float2(sum[0].x + sum[0].y, 0.f), p.warps).x * p.inv_c;
     if (me.t == 0 && ok && row + p.slots * step < p.total) {     // every thread of the row has read its slot
       const T* src[1] = {source(row + p.slots * step)};
       ring.issue(ring.slot, src);
     }
-    float sq = 0.f;
+    const float2 nm = both(-mean);
+    float2 sq[2] = {both(0.f), both(0.f)};
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       opaque(v[k]);                    // convert again instead of keeping fp32 copies
-      if ((me.t + k * me.threads) * VEC >= p.C) continue;
+      const Piece<CONTIG> at(me.t, k, me.threads, p.C);
+      if (!at.any()) continue;
+      float2 f[2];
+      pairs<T>(v[k], f);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float d = to_f32(v[k].v[e]) - mean;
-        sq += d * d;
+      for (int e = 0; e < 2; ++e) {
+        float2 d = fadd2(f[e], nm);
+        if (!at.has(2 * e)) d.x = 0.f;
+        if (!at.has(2 * e + 1)) d.y = 0.f;
+        sq[e & 1] = ffma2(d, d, sq[e & 1]);
       }
     }
-    const float rstd = 1.0f / sqrtf(me.sum(make_float2(sq, 0.f), p.warps).x * p.inv_c + p.eps);
+    sq[0] = fadd2(sq[0], sq[1]);
+    const float rstd = 1.0f / sqrtf(me.sum(make_float2(sq[0].x + sq[0].y, 0.f), p.warps).x * p.inv_c + p.eps);
     if (!ok) continue;
     T* y = static_cast<T*>(p.y) + s * p.y_batch + i * p.y_row;
     const W* w = p.w ? static_cast<const W*>(p.w) + s * p.w_batch : nullptr;
@@ -218,15 +291,19 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormArgs p) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       opaque(v[k]);
-      const int c = (me.t + k * me.threads) * VEC;
-      if (c >= p.C) continue;
-      float wv[VEC], bv[VEC];
-      if (w) load_f32<W, VEC>(w + c, wv);
-      if (b) load_f32<W, VEC>(b + c, bv);
+      const Piece<CONTIG> at(me.t, k, me.threads, p.C);
+      if (!at.any()) continue;
+      float2 f[2], wv[2], bv[2];
+      pairs<T>(v[k], f);
+      if (w) pairs<W>(at.load(w), wv);
+      if (b) pairs<W>(at.load(b), bv);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        v[k].v[e] = from_f32<T>((to_f32(v[k].v[e]) - mean) * rstd * (w ? wv[e] + p.plus : 1.0f) + (b ? bv[e] : 0.0f));
-      *reinterpret_cast<Vec<T, VEC>*>(y + c) = v[k];
+      for (int e = 0; e < 2; ++e) {
+        f[e] = fmul2(fadd2(f[e], nm), both(rstd));
+        f[e] = ffma2(f[e], w ? fadd2(wv[e], both(p.plus)) : both(1.0f), b ? bv[e] : both(0.f));
+      }
+      unpairs<T>(v[k], f);
+      at.store(y, v[k]);
     }
     if (me.t == 0) {
       if (p.mean) p.mean[row] = mean;
@@ -237,13 +314,12 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormArgs p) {
 }
 
 // One block walks the rows [r0, r1) of run blockIdx.x, its row groups in turn.
-template <typename T, typename W, int VEC, int NV, bool MULTI>
+template <typename T, typename W, bool CONTIG, int NV, bool MULTI>
 __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormArgs p) {
   __shared__ float2 red[64];
   __shared__ uint64_t bars[kBars];
   __shared__ uint32_t abort_word;
   extern __shared__ __align__(16) uint8_t smem[];
-  float* acc = reinterpret_cast<float*>(smem);       // [2][C] at the end, when a block holds several rows
   init_bars(bars, &abort_word, p.at_once * p.slots);
   Row<MULTI> me(p, red);
   Ring<T, 2> ring(p, me.group, bars, smem, &abort_word);
@@ -251,11 +327,11 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormArgs p) {
   const int64_t run = blockIdx.x - group * p.runs_per_group;
   const int64_t r0 = group * p.group_rows + p.group_rows * run / p.runs_per_group;
   const int64_t r1 = group * p.group_rows + p.group_rows * (run + 1) / p.runs_per_group;
-  float dw[NV][VEC], db[NV][VEC];
+  float2 dw[NV][2], db[NV][2];
 #pragma unroll
   for (int k = 0; k < NV; ++k)
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) dw[k][e] = db[k][e] = 0.f;
+    for (int e = 0; e < 2; ++e) dw[k][e] = db[k][e] = both(0.f);
   auto issue = [&](int slot, int64_t row) {
     const uint32_t s = p.div_rows.div((uint32_t)row), i = (uint32_t)row - s * p.rows;
     const T* src[2] = {static_cast<const T*>(p.x) + s * p.x_batch + i * p.x_row,
@@ -264,83 +340,99 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormArgs p) {
   };
   if (me.t == 0)
     for (int k = 0; k < p.slots && r0 + me.group + k * p.at_once < r1; ++k) issue(k, r0 + me.group + k * p.at_once);
+  float mean = 0.f, rstd = 0.f;        // of the next row
+  if (r0 + me.group < r1) {
+    mean = __ldg(p.mean + r0 + me.group);
+    rstd = __ldg(p.rstd + r0 + me.group);
+  }
   for (int64_t row = r0 + me.group; row < r1; row += p.at_once, ring.next()) {
     const uint32_t s = p.div_rows.div((uint32_t)row), i = (uint32_t)row - s * p.rows;
     const T* x = ring.row(0, static_cast<const T*>(p.x) + s * p.x_batch + i * p.x_row);
     const T* dy = ring.row(1, static_cast<const T*>(p.dy) + s * p.dy_batch + i * p.dy_row);
-    const float mean = __ldg(p.mean + row), rstd = __ldg(p.rstd + row);
-    const bool ok = ring.wait();       // (after one that ran out the rows' barriers are still kept)
     const W* w = p.w ? static_cast<const W*>(p.w) + s * p.w_batch : nullptr;
-    Vec<T, VEC> xv[NV], gv[NV];
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int c = (me.t + k * me.threads) * VEC;
-      const bool in = c < p.C;
-      xv[k] = in ? *reinterpret_cast<const Vec<T, VEC>*>(x + c) : Vec<T, VEC>{};
-      gv[k] = in ? *reinterpret_cast<const Vec<T, VEC>*>(dy + c) : Vec<T, VEC>{};
+    const float2 nm = both(-mean), rs = both(rstd), plus = both(p.plus);
+    if (row + p.at_once < r1) {
+      mean = __ldg(p.mean + row + p.at_once);
+      rstd = __ldg(p.rstd + row + p.at_once);
     }
-    float a = 0.f, b = 0.f;
+    const bool ok = ring.wait();       // (after one that ran out the rows' barriers are still kept)
+    Vec<T, 4> xv[NV], gv[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int c = (me.t + k * me.threads) * VEC;
-      if (c >= p.C) continue;
-      float wv[VEC];
-      if (w) load_f32<W, VEC>(w + c, wv);
+      const Piece<CONTIG> at(me.t, k, me.threads, p.C);
+      xv[k] = at.load(x);
+      gv[k] = at.load(dy);
+    }
+    float2 a = both(0.f), b = both(0.f);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float xh = (to_f32(xv[k].v[e]) - mean) * rstd;
-        float g = to_f32(gv[k].v[e]);
-        dw[k][e] += g * xh;
-        db[k][e] += g;
-        if (w) g *= wv[e] + p.plus;
-        a += g;
-        b += g * xh;
+    for (int k = 0; k < NV; ++k) {
+      const Piece<CONTIG> at(me.t, k, me.threads, p.C);
+      if (!at.any()) continue;
+      float2 xf[2], gf[2], wv[2];
+      pairs<T>(xv[k], xf);
+      pairs<T>(gv[k], gf);
+      if (w) pairs<W>(at.load(w), wv);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float2 xh = fmul2(fadd2(xf[e], nm), rs);
+        dw[k][e] = ffma2(gf[e], xh, dw[k][e]);
+        db[k][e] = fadd2(db[k][e], gf[e]);
+        const float2 g = w ? fmul2(gf[e], fadd2(wv[e], plus)) : gf[e];
+        a = fadd2(a, g);
+        b = ffma2(g, xh, b);
       }
     }
-    const float2 ab = me.sum(make_float2(a, b), p.warps);
+    const float2 ab = me.sum(make_float2(a.x + a.y, b.x + b.y), p.warps);
     if (me.t == 0 && ok && row + (int64_t)p.slots * p.at_once < r1) issue(ring.slot, row + (int64_t)p.slots * p.at_once);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {     // convert again below instead of keeping fp32 copies
       opaque(xv[k]);
       opaque(gv[k]);
     }
-    const float am = ab.x * p.inv_c, bm = ab.y * p.inv_c;
+    const float2 am = both(-ab.x * p.inv_c), bm = both(-ab.y * p.inv_c);
     if (!ok) continue;
     T* dx = static_cast<T*>(p.y) + s * p.y_batch + i * p.y_row;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int c = (me.t + k * me.threads) * VEC;
-      if (c >= p.C) continue;
-      float wv[VEC];
-      if (w) load_f32<W, VEC>(w + c, wv);           // (again: cheaper than keeping g in fp32)
+      const Piece<CONTIG> at(me.t, k, me.threads, p.C);
+      if (!at.any()) continue;
+      float2 xf[2], gf[2], wv[2];
+      pairs<T>(xv[k], xf);
+      pairs<T>(gv[k], gf);
+      if (w) pairs<W>(at.load(w), wv);       // (again: cheaper than keeping g in fp32)
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float xh = (to_f32(xv[k].v[e]) - mean) * rstd;
-        const float g = to_f32(gv[k].v[e]) * (w ? wv[e] + p.plus : 1.0f);
-        gv[k].v[e] = from_f32<T>(rstd * (g - am - xh * bm));
+      for (int e = 0; e < 2; ++e) {
+        const float2 xh = fmul2(fadd2(xf[e], nm), rs);
+        const float2 g = w ? fmul2(gf[e], fadd2(wv[e], plus)) : gf[e];
+        xf[e] = fmul2(rs, ffma2(xh, bm, fadd2(g, am)));
       }
-      *reinterpret_cast<Vec<T, VEC>*>(dx + c) = gv[k];
+      unpairs<T>(gv[k], xf);
+      at.store(dx, gv[k]);
     }
   }
   report(&abort_word);
   if (!p.part) return;
+  // the row groups hold sums of the same columns: side by side in the slots' memory, then added in order
   float* out = p.part + (int64_t)blockIdx.x * 2 * p.C;
-  if (p.at_once > 1) __syncthreads();  // the slots' memory is used again
-  // the block's row groups hold sums of the same columns: add them in order
-  for (int q = 0; q < p.at_once; ++q) {
-    if (me.group == q) {
-      float* to = p.at_once > 1 && q + 1 < p.at_once ? acc : out;
+  float* acc = reinterpret_cast<float*>(smem);           // [at_once][2][C]
+  float* mine = p.at_once > 1 ? acc + (int64_t)me.group * 2 * p.C : out;
+  __syncthreads();
 #pragma unroll
-      for (int k = 0; k < NV; ++k)
+  for (int k = 0; k < NV; ++k) {
+    const Piece<CONTIG> at(me.t, k, me.threads, p.C);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const int c = (me.t + k * me.threads) * VEC + e;
-          if (c >= p.C) continue;
-          to[c] = dw[k][e] + (q ? acc[c] : 0.f);
-          to[p.C + c] = db[k][e] + (q ? acc[p.C + c] : 0.f);
-        }
+    for (int e = 0; e < 4; ++e) {
+      if (at.at(e) >= p.C) continue;
+      mine[at.at(e)] = e & 1 ? dw[k][e / 2].y : dw[k][e / 2].x;
+      mine[p.C + at.at(e)] = e & 1 ? db[k][e / 2].y : db[k][e / 2].x;
     }
-    if (p.at_once > 1) __syncthreads();
+  }
+  if (p.at_once == 1) return;
+  __syncthreads();
+  for (int c = threadIdx.x; c < 2 * p.C; c += blockDim.x) {
+    float t = acc[c];
+    for (int q = 1; q < p.at_once; ++q) t += acc[(int64_t)q * 2 * p.C + c];
+    out[c] = t;
   }
 }
 
@@ -363,23 +455,20 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* part, in
   if (threadIdx.x == 0 && col < C) out[g * C + col] = from_f32<O>(s);
 }
 
-// How a row is spread: its warps and its vectors per lane, of `most` at most.
+// How a row is spread: its warps and its pieces of four elements per lane, at most 16 of 16 bits and 8 of
+// 32 bits or not contiguous; in the backward pass, with two sums beside each element, 6 and 4.  The
+// widest rows take 8, so that 16 warps hold them.
 struct Spread {
   int warps, nv;
 };
-Spread spread(int C, int vec, int most) {
-  const int pieces = (C + vec - 1) / vec;                  // vectors of a row
+Spread spread(bool bwd, bool contig, int C, int elem) {
+  const bool light = contig && elem == 2;
+  const int most = !bwd ? (light ? 16 : 8) : (C <= 8192 ? (light ? 6 : 4) : 8);
+  const int pieces = (C + 3) / 4;
   const int warps = (pieces + 32 * most - 1) / (32 * most);
   return {warps, (pieces + 32 * warps - 1) / (32 * warps)};
 }
-// Vectors per lane at most: 64 elements of 16 bits, 32 of 32 bits; the backward pass, with two sums
-// beside each element, 24 and 16; one by one (unaligned rows) 16.  The widest rows take 32 elements,
-// so that 16 warps hold them.
-int most_vectors(bool bwd, int vec, int C) {
-  if (vec == 8) return bwd ? (C <= 12288 ? 3 : 4) : 8;
-  if (vec == 4) return bwd && C <= 8192 ? 4 : 8;
-  return C <= 8192 ? 16 : 32;
-}
+
 constexpr int kSmem = 200 * 1024;      // dynamic shared memory of a block at most
 
 // Rows of a block at a time (16 warps, one block per multiprocessor; named barriers give 15 groups of
@@ -391,12 +480,12 @@ void plan_block(NormArgs& a, bool bwd, int elem, int64_t rows_per_block) {
   a.at_once = a.warps > 1 ? std::min(15, 16 / a.warps) : 16;
   a.at_once = (int)std::max<int64_t>(1, std::min<int64_t>(a.at_once, rows_per_block));
   a.at_once = std::min(a.at_once, std::max(1, kSmem / (tensors * a.slot_bytes)));
-  if (bwd && 2 * a.C * (int)sizeof(float) > kSmem) a.at_once = 1;
+  if (bwd) a.at_once = std::min(a.at_once, std::max(1, kSmem / (2 * a.C * (int)sizeof(float))));
   a.slots = std::max(1, std::min(8, kSmem / (a.at_once * tensors * a.slot_bytes)));
 }
 int smem_bytes(const NormArgs& a, bool bwd) {
   const int ring = a.at_once * a.slots * (bwd ? 2 : 1) * a.slot_bytes;
-  return std::max(ring, bwd && a.at_once > 1 ? 2 * a.C * (int)sizeof(float) : 0);
+  return std::max(ring, bwd && a.at_once > 1 ? a.at_once * 2 * a.C * (int)sizeof(float) : 0);
 }
 
 // Runs of a group in the backward pass: one block per multiprocessor, no more than rows.
@@ -414,51 +503,42 @@ cudaError_t launch_one(K kernel, int blocks, int threads, int smem, const NormAr
   return cudaGetLastError();
 }
 
-template <typename T, typename W, int VEC, int NV>
+template <typename T, typename W, bool CONTIG, int NV>
 cudaError_t launch_nv(bool bwd, const NormArgs& a, int blocks, cudaStream_t st) {
   const int threads = 32 * a.warps * a.at_once, smem = smem_bytes(a, bwd);
   if (!bwd)
-    return a.warps > 1 ? launch_one(norm_fwd_kernel<T, W, VEC, NV, true>, blocks, threads, smem, a, st)
-                       : launch_one(norm_fwd_kernel<T, W, VEC, NV, false>, blocks, threads, smem, a, st);
-  if constexpr (VEC * NV <= 32)                            // (no wider: see most_vectors)
-    return a.warps > 1 ? launch_one(norm_bwd_kernel<T, W, VEC, NV, true>, blocks, threads, smem, a, st)
-                       : launch_one(norm_bwd_kernel<T, W, VEC, NV, false>, blocks, threads, smem, a, st);
+    return a.warps > 1 ? launch_one(norm_fwd_kernel<T, W, CONTIG, NV, true>, blocks, threads, smem, a, st)
+                       : launch_one(norm_fwd_kernel<T, W, CONTIG, NV, false>, blocks, threads, smem, a, st);
+  if constexpr (NV <= 8)                                   // (no more: see spread)
+    return a.warps > 1 ? launch_one(norm_bwd_kernel<T, W, CONTIG, NV, true>, blocks, threads, smem, a, st)
+                       : launch_one(norm_bwd_kernel<T, W, CONTIG, NV, false>, blocks, threads, smem, a, st);
   return cudaErrorInvalidValue;
 }
 
-template <typename T, typename W, int VEC>
-cudaError_t launch_vec(bool bwd, const NormArgs& a, int nv, int blocks, cudaStream_t st) {
-  if constexpr (VEC == 1) {
-    return nv <= 4 ? launch_nv<T, W, 1, 4>(bwd, a, blocks, st) : nv <= 8  ? launch_nv<T, W, 1, 8>(bwd, a, blocks, st)
-           : nv <= 16 ? launch_nv<T, W, 1, 16>(bwd, a, blocks, st)
-                      : launch_nv<T, W, 1, 32>(bwd, a, blocks, st);
-  } else {
-    switch (nv) {
-      case 1: return launch_nv<T, W, VEC, 1>(bwd, a, blocks, st);
-      case 2: return launch_nv<T, W, VEC, 2>(bwd, a, blocks, st);
-      case 3: return launch_nv<T, W, VEC, 3>(bwd, a, blocks, st);
-      default: break;
-    }
-    if (nv <= 4) return launch_nv<T, W, VEC, 4>(bwd, a, blocks, st);
-    if (nv <= 6) return launch_nv<T, W, VEC, 6>(bwd, a, blocks, st);
-    return launch_nv<T, W, VEC, 8>(bwd, a, blocks, st);
-  }
+template <typename T, typename W, bool CONTIG>
+cudaError_t launch_pieces(bool bwd, const NormArgs& a, int nv, int blocks, cudaStream_t st) {
+  return nv <= 2    ? launch_nv<T, W, CONTIG, 2>(bwd, a, blocks, st)
+         : nv <= 4  ? launch_nv<T, W, CONTIG, 4>(bwd, a, blocks, st)
+         : nv <= 6  ? launch_nv<T, W, CONTIG, 6>(bwd, a, blocks, st)
+         : nv <= 8  ? launch_nv<T, W, CONTIG, 8>(bwd, a, blocks, st)
+         : nv <= 12 ? launch_nv<T, W, CONTIG, 12>(bwd, a, blocks, st)
+                    : launch_nv<T, W, CONTIG, 16>(bwd, a, blocks, st);
 }
 
 template <typename T, typename W>
-cudaError_t launch_norm(bool bwd, int vec, const NormArgs& a, int nv, int blocks, cudaStream_t st) {
-  return vec > 1 ? launch_vec<T, W, (int)(16 / sizeof(T))>(bwd, a, nv, blocks, st) : launch_vec<T, W, 1>(bwd, a, nv, blocks, st);
+cudaError_t launch_norm(bool bwd, bool contig, const NormArgs& a, int nv, int blocks, cudaStream_t st) {
+  return contig ? launch_pieces<T, W, true>(bwd, a, nv, blocks, st) : launch_pieces<T, W, false>(bwd, a, nv, blocks, st);
 }
 
-cudaError_t dispatch(bool bwd, int dtype, int wdtype, int vec, const NormArgs& a, int nv, int blocks, cudaStream_t st) {
+cudaError_t dispatch(bool bwd, int dtype, int wdtype, bool contig, const NormArgs& a, int nv, int blocks, cudaStream_t st) {
   const bool wf = wdtype == ULTRAGEN_F32;
   if (dtype == ULTRAGEN_BF16)
-    return wf ? launch_norm<__nv_bfloat16, float>(bwd, vec, a, nv, blocks, st)
-              : launch_norm<__nv_bfloat16, __nv_bfloat16>(bwd, vec, a, nv, blocks, st);
+    return wf ? launch_norm<__nv_bfloat16, float>(bwd, contig, a, nv, blocks, st)
+              : launch_norm<__nv_bfloat16, __nv_bfloat16>(bwd, contig, a, nv, blocks, st);
   if (dtype == ULTRAGEN_F16)
-    return wf ? launch_norm<__half, float>(bwd, vec, a, nv, blocks, st)
-              : launch_norm<__half, __half>(bwd, vec, a, nv, blocks, st);
-  return launch_norm<float, float>(bwd, vec, a, nv, blocks, st);
+    return wf ? launch_norm<__half, float>(bwd, contig, a, nv, blocks, st)
+              : launch_norm<__half, __half>(bwd, contig, a, nv, blocks, st);
+  return launch_norm<float, float>(bwd, contig, a, nv, blocks, st);
 }
 
 int elem_size(int dtype) { return dtype == ULTRAGEN_F32 ? 4 : 2; }
@@ -473,10 +553,10 @@ int check(const ultragen_norm_t* n) {
   return ULTRAGEN_OK;
 }
 
-// Whether a row operand can be read 16 bytes at a time.
-bool rows16(const void* p, int64_t row, int64_t batch, int vec, int dtype) {
-  return p == nullptr || (((uintptr_t)p & 15u) == 0 && row * elem_size(dtype) % 16 == 0 &&
-                          batch * elem_size(dtype) % 16 == 0 && vec > 1);
+// Whether an operand's rows start on `bytes`.
+bool starts_on(const void* p, int64_t row, int64_t batch, int bytes, int dtype) {
+  const int e = elem_size(dtype);
+  return p == nullptr || ((uintptr_t)p % bytes == 0 && row * e % bytes == 0 && batch * e % bytes == 0);
 }
 
 NormArgs args_of(const ultragen_norm_t* n) {
@@ -499,17 +579,15 @@ NormArgs args_of(const ultragen_norm_t* n) {
   return a;
 }
 
-// 16-byte vectors need every row, and every sample's weight, to start on a 16-byte boundary (a
-// weight wider than the rows then does too, its vectors being a multiple of theirs).  Returns the
-// elements of a vector, 1 without.
-int vectorised(const ultragen_norm_t* n, const void* x, const void* dy, const void* y, const void* w,
-                const void* b) {
-  const int vec = 16 / elem_size(n->dtype);
+// Whether every row, and every sample's weight, starts on four elements.
+bool contiguous_pieces(const ultragen_norm_t* n, const void* x, const void* dy, const void* y, const void* w,
+               const void* b) {
+  const int e = 4 * elem_size(n->dtype), we = 4 * elem_size(n->wdtype);
   const int64_t wb = n->per_sample ? n->cols : 0;
-  const bool ok = n->cols % vec == 0 && rows16(x, n->x_row, n->x_batch, vec, n->dtype) &&
-         rows16(dy, n->dy_row, n->dy_batch, vec, n->dtype) && rows16(y, n->y_row, n->y_batch, vec, n->dtype) &&
-         rows16(w, wb, wb, vec, n->wdtype) && rows16(b, wb, wb, vec, n->wdtype);
-  return ok ? vec : 1;
+  return n->cols % 4 == 0 && starts_on(x, n->x_row, n->x_batch, e, n->dtype) &&
+         starts_on(dy, n->dy_row, n->dy_batch, e, n->dtype) &&
+         starts_on(y, n->y_row, n->y_batch, e, n->dtype) && starts_on(w, wb, wb, we, n->wdtype) &&
+         starts_on(b, wb, wb, we, n->wdtype);
 }
 
 int status_of(cudaError_t e) { return e == cudaSuccess ? ULTRAGEN_OK : ULTRAGEN_ERR_CUDA; }
@@ -540,12 +618,12 @@ int ultragen_layer_norm(const ultragen_norm_t* n, const void* x, const void* wei
   a.y = y;
   a.mean = mean;
   a.rstd = rstd;
-  const int vec = vectorised(n, x, nullptr, y, weight, bias);
-  const Spread sp = spread(n->cols, vec, most_vectors(false, vec, n->cols));
+  const bool contig = contiguous_pieces(n, x, nullptr, y, weight, bias);
+  const Spread sp = spread(false, contig, n->cols, elem_size(n->dtype));
   a.warps = sp.warps;
   plan_block(a, false, elem_size(n->dtype), (a.total + sm_count() - 1) / sm_count());
   const int64_t blocks = std::min<int64_t>((a.total + a.at_once - 1) / a.at_once, sm_count());
-  return status_of(dispatch(false, n->dtype, n->wdtype, vec, a, sp.nv, (int)blocks,
+  return status_of(dispatch(false, n->dtype, n->wdtype, contig, a, sp.nv, (int)blocks,
                             reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -580,8 +658,8 @@ int ultragen_layer_norm_backward(const ultragen_norm_t* n, const void* dy, const
   }
   if (!dy || !x || !mean || !rstd || !dx) return ULTRAGEN_ERR_INVALID_ARG;
   if ((st = current_device(&dev)) != ULTRAGEN_OK) return st;
-  const int vec = vectorised(n, x, dy, dx, weight, nullptr);
-  const Spread sp = spread(n->cols, vec, most_vectors(true, vec, n->cols));
+  const bool contig = contiguous_pieces(n, x, dy, dx, weight, nullptr);
+  const Spread sp = spread(true, contig, n->cols, elem_size(n->dtype));
   a.warps = sp.warps;
   a.runs_per_group = runs_of(a.group_rows, groups, sm_count());
   plan_block(a, true, elem_size(n->dtype), (a.group_rows + a.runs_per_group - 1) / a.runs_per_group);
@@ -597,7 +675,7 @@ int ultragen_layer_norm_backward(const ultragen_norm_t* n, const void* dy, const
   a.mean = const_cast<float*>(mean);
   a.rstd = const_cast<float*>(rstd);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  st = status_of(dispatch(true, n->dtype, n->wdtype, vec, a, sp.nv, (int)(groups * a.runs_per_group), s));
+  st = status_of(dispatch(true, n->dtype, n->wdtype, contig, a, sp.nv, (int)(groups * a.runs_per_group), s));
   if (st != ULTRAGEN_OK || !a.part) return st;
   const dim3 grid((n->cols + 31) / 32, (unsigned)groups, 2), block(32, 32);
   if (grad_dtype == ULTRAGEN_F32)
