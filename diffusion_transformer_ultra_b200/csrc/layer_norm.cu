@@ -7,17 +7,18 @@
 //   dw = sum over rows of dy xh,   db = sum over rows of dy
 //
 // Both passes are bound by HBM: x is read and y written once (x, dy read and dx written once).
-// A row belongs to one warp up to 2,048 elements of 16 bits (1,024 of 32; the backward pass, which
-// keeps the weight's gradient too, fewer), else to a group of warps.  Its rows come by bulk copies,
-// several ahead, into shared memory (a persistent block per multiprocessor has up to 200 KB of them in
-// flight), and from there to registers, as they were read, so that the variance takes a second pass
-// over registers (no cancellation of sum(x^2) against mu^2).  A copy covers the 16-byte pieces that
-// hold the row, so that a row may start anywhere; one that does not start on four elements is then
-// worked on element by element.  All sums are fp32.
-// With the loads ahead of time the instructions and the weight's way from L1 set the pace: arithmetic
-// is on pairs, and a lane's piece is four elements, so that a warp's fp32 weights are one contiguous
-// 512-byte load.  (With pieces of eight, whose fp32 weights a warp reads in halves of 32-byte sectors,
-// and scalar arithmetic, the forward pass took 150 instead of 1XX us for 70,144 x 2,048 bf16.)
+// A row belongs to a group of as many warps as give each lane 16 elements (32 in the widest rows), so
+// that the lane's part of the weight and bias stays in registers from row to row.  Rows come by bulk
+// copies, several ahead, into shared memory (a persistent block per multiprocessor has up to 200 KB of
+// them in flight), and from there to registers, so that the variance takes a second pass over registers
+// (no cancellation of sum(x^2) against mu^2).  A copy covers the 16-byte pieces that hold the row, so
+// that a row may start anywhere; one that does not start on four elements is then worked on element by
+// element.  All sums are fp32, the arithmetic is on pairs.
+// With the loads out of the way a row is one chain of dependent steps, and what the chain holds sets the
+// pace: a warp of its own issues the copies, and a row group of the forward pass takes two rows at a
+// time, whose sums share the shuffles and barriers.  For 70,144 x 2,048 bf16 with fp32 weights that
+// takes 150 us; a row group that issues its own copies 158; a row to a block, loads straight to
+// registers, 151; and the kernel for such rows below, 122 (a copy of the same bytes takes 94).
 //
 // The weight's gradient: a block of the backward pass walks a run of rows of one sample (of the
 // whole batch with a shared weight), keeps its columns' sums in registers, and writes them once
@@ -60,6 +61,7 @@ struct NormArgs {
   int runs_per_group;      // runs of a sample (of everything with a shared weight)
   int64_t group_rows;      // rows of a sample (of everything with a shared weight)
   int warps;               // warps of a row
+  int wide;                // forward: norm_wide_kernel
   int at_once;             // rows of a block at a time
   int slots, slot_bytes;   // rows in flight per row group; bytes of one tensor's row in a slot
   float plus, inv_c, eps;
@@ -88,9 +90,13 @@ struct Row {
     flip ^= 1;
     if (lane == 0) buf[t >> 5] = x;
     asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(threads) : "memory");
-    x = lane < warps ? buf[lane] : make_float2(0.f, 0.f);
-    x.x = warp_sum(x.x);
-    x.y = warp_sum(x.y);
+    x = make_float2(0.f, 0.f);
+    for (int q = 0; q < warps; q += 4) {
+      float2 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = q + i < warps ? buf[q + i] : make_float2(0.f, 0.f);
+      x = fadd2(x, fadd2(fadd2(v[0], v[1]), fadd2(v[2], v[3])));
+    }
     return x;
   }
 };
@@ -102,12 +108,12 @@ constexpr uint32_t kWaitNs = 2000u * 1000 * 1000;
 // The rows of one row group on their way through shared memory: `slots` slots of N tensors' rows each.
 template <typename T, int N>
 struct Ring {
-  uint32_t bar, abort_word;            // barriers of this group's slots
+  uint32_t bar, abort_word;            // barriers of this group's slots: full, then empty
   uint8_t* buf;
   int slots, slot_bytes, row_bytes, slot;
   uint32_t phase;
   __device__ __forceinline__ Ring(const NormArgs& p, int group, uint64_t* bars, uint8_t* smem, uint32_t* abort)
-      : bar(smem_u32(bars + group * p.slots)), abort_word(smem_u32(abort)),
+      : bar(smem_u32(bars + 2 * group * p.slots)), abort_word(smem_u32(abort)),
         buf(smem + (int64_t)group * p.slots * N * p.slot_bytes), slots(p.slots), slot_bytes(p.slot_bytes),
         row_bytes(p.C * (int)sizeof(T)), slot(0), phase(0) {}
   // One thread: the 16-byte pieces that hold the rows at src[0 .. N) into slot `to`.
@@ -132,6 +138,12 @@ struct Ring {
   __device__ __forceinline__ const T* row(int i, const T* src) const {
     return reinterpret_cast<const T*>(buf + (slot * N + i) * slot_bytes + ((uint32_t)(uintptr_t)src & 15u));
   }
+  // The current slot may be written again (one thread, when all of the row have read it).
+  __device__ __forceinline__ void release(int s) const { mbar_arrive(bar + 8 * (slots + s)); }
+  // The producer's side: waits until the current slot is free.
+  __device__ __forceinline__ bool wait_free() const {
+    return mbar_wait_short(bar + 8 * (slots + slot), phase ^ 1, abort_word, DEV_TIMEOUT_PRODUCER, kWaitNs);
+  }
   __device__ __forceinline__ void next() {
     if (++slot == slots) {
       slot = 0;
@@ -140,8 +152,8 @@ struct Ring {
   }
 };
 
-// Barriers of a block's slots (at most kBars in all).
-constexpr int kBars = 128;
+// Barriers of a block's slots (at most kBars / 2 slots in all).
+constexpr int kBars = 256;
 __device__ __forceinline__ void init_bars(uint64_t* bars, uint32_t* abort, int n) {
   for (int i = threadIdx.x; i < n; i += blockDim.x) mbar_init(smem_u32(bars + i), 1);
   if (threadIdx.x == 0) *abort = 0;
@@ -155,262 +167,455 @@ __device__ __forceinline__ void report(const uint32_t* abort) {
   settle();
 }
 
-// The vector's registers as values the compiler knows nothing about.
+// A piece: four elements of a row, as 32-bit words (kept as such: element by element, the compiler
+// takes 16-bit types apart and together again).
 template <typename T>
-__device__ __forceinline__ void opaque(Vec<T, 4>& v) {
-#pragma unroll
-  for (int i = 0; i < (int)sizeof(T); ++i) asm volatile("" : "+r"(reinterpret_cast<uint32_t*>(&v)[i]));
-}
-
-// A piece: four elements of a row, as fp32 pairs.
+struct Raw {
+  uint32_t w[sizeof(T)];
+};
 template <typename T>
-__device__ __forceinline__ void pairs(const Vec<T, 4>& v, float2 (&out)[2]) {
+__device__ __forceinline__ void pairs(const Raw<T>& v, float2 (&out)[2]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    if constexpr (sizeof(T) == 4) {
-      out[i] = make_float2(v.v[2 * i], v.v[2 * i + 1]);
-    } else if constexpr (std::is_same<T, __half>::value) {
-      out[i] = __half22float2(reinterpret_cast<const __half2*>(&v)[i]);
-    } else {
-      const uint32_t w = reinterpret_cast<const uint32_t*>(&v)[i];
-      out[i] = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-    }
+    if constexpr (sizeof(T) == 4) out[i] = make_float2(__uint_as_float(v.w[2 * i]), __uint_as_float(v.w[2 * i + 1]));
+    else if constexpr (std::is_same<T, __half>::value) out[i] = __half22float2(*reinterpret_cast<const __half2*>(&v.w[i]));
+    else out[i] = make_float2(__uint_as_float(v.w[i] << 16), __uint_as_float(v.w[i] & 0xffff0000u));
   }
 }
 template <typename T>
-__device__ __forceinline__ void unpairs(Vec<T, 4>& v, const float2 (&in)[2]) {
+__device__ __forceinline__ void unpairs(Raw<T>& v, const float2 (&in)[2]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     if constexpr (sizeof(T) == 4) {
-      v.v[2 * i] = in[i].x;
-      v.v[2 * i + 1] = in[i].y;
+      v.w[2 * i] = __float_as_uint(in[i].x);
+      v.w[2 * i + 1] = __float_as_uint(in[i].y);
     } else {
-      reinterpret_cast<uint32_t*>(&v)[i] = pack2<T>(in[i].x, in[i].y);
+      v.w[i] = pack2<T>(in[i].x, in[i].y);
     }
   }
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
-// Piece k of thread t of a row's `threads`: columns 4 (t + k threads) and on where rows start on four
-// elements (CONTIG; C is then a multiple of four), else t + (4 k + e) threads, element by element.
-template <bool CONTIG>
-struct Piece {
-  int col, step, C;
-  __device__ __forceinline__ Piece(int t, int k, int threads, int C_)
-      : col(CONTIG ? (t + k * threads) * 4 : t + 4 * k * threads), step(CONTIG ? 1 : threads), C(C_) {}
-  __device__ __forceinline__ bool any() const { return col < C; }
-  __device__ __forceinline__ int at(int e) const { return col + e * step; }
-  __device__ __forceinline__ bool has(int e) const { return CONTIG || at(e) < C; }
+// The words as values the compiler knows nothing about.
+template <typename T>
+__device__ __forceinline__ void opaque(Raw<T>& v) {
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T); ++i) asm volatile("" : "+r"(v.w[i]));
+}
+
+// A lane's pieces of a row.  Warp q of the row has the span of 128 NV columns from 128 NV q; its piece k
+// is four columns in a row, 128 k + 4 lane, where rows start on four elements (CONTIG; C is then a
+// multiple of four), else 128 k + lane + 32 e.  The offsets within the span are constants, and only the
+// row's last warp (`full` false) looks at the row's end.
+template <bool CONTIG, int NV>
+struct Span {
+  int col, C;                          // this lane's first column
+  bool full;
+  __device__ __forceinline__ Span(int t, int C_) : C(C_) {
+    const int first = (t >> 5) * (NV * 128);
+    col = first + (CONTIG ? 4 : 1) * (t & 31);
+    full = first + NV * 128 <= C;
+  }
+  static __device__ constexpr int offset(int k, int e) { return k * 128 + (CONTIG ? e : 32 * e); }
+  __device__ __forceinline__ bool has(int k, int e) const { return full || col + offset(k, e) < C; }
+  // From shared memory, which may be read behind the row's end: zeros there.
   template <typename T>
-  __device__ __forceinline__ Vec<T, 4> load(const T* p) const {   // zeros behind the row
-    Vec<T, 4> v{};
-    if (CONTIG) {
-      if (any()) v = *reinterpret_cast<const Vec<T, 4>*>(p + col);
+  __device__ __forceinline__ void load_row(const T* row, Raw<T> (&v)[NV]) const {
+    const T* p = row + col;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) v[k] = words(p + offset(k, 0), [&](int e) { return offset(0, e); });
+    if (full) return;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[k].w[e] = has(k, e) ? v[k].w[e] : 0u;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          v[k].w[i] &= (has(k, 2 * i) ? 0xffffu : 0u) | (has(k, 2 * i + 1) ? 0xffff0000u : 0u);
+      }
+    }
+  }
+  // From global memory: some elements of the row behind its end.
+  template <typename T>
+  __device__ __forceinline__ Raw<T> load_any(const T* row, int k) const {
+    const int c = col + offset(k, 0);
+    if (CONTIG) return words(row + min(c, C - 4), [](int e) { return e; });
+    return words(row, [&](int e) { return min(c + 32 * e, C - 1); });
+  }
+  template <typename T>
+  __device__ __forceinline__ void store(T* row, int k, const Raw<T>& v) const {
+    T* p = row + col + offset(k, 0);
+    if constexpr (CONTIG && sizeof(T) == 4) {
+      if (has(k, 0)) *reinterpret_cast<uint4*>(p) = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+    } else if constexpr (CONTIG) {
+      if (has(k, 0)) *reinterpret_cast<uint2*>(p) = make_uint2(v.w[0], v.w[1]);
     } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (has(e)) v.v[e] = p[at(e)];
+      for (int e = 0; e < 4; ++e) {
+        if (!has(k, e)) continue;
+        if constexpr (sizeof(T) == 4) reinterpret_cast<uint32_t*>(p)[32 * e] = v.w[e];
+        else reinterpret_cast<uint16_t*>(p)[32 * e] = (uint16_t)(v.w[e >> 1] >> (16 * (e & 1)));
+      }
+    }
+  }
+
+ private:
+  template <typename T, typename At>
+  static __device__ __forceinline__ Raw<T> words(const T* p, At at) {
+    Raw<T> v;
+    if constexpr (CONTIG && sizeof(T) == 4) {
+      const uint4 u = *reinterpret_cast<const uint4*>(p);
+      v.w[0] = u.x;
+      v.w[1] = u.y;
+      v.w[2] = u.z;
+      v.w[3] = u.w;
+    } else if constexpr (CONTIG) {
+      const uint2 u = *reinterpret_cast<const uint2*>(p);
+      v.w[0] = u.x;
+      v.w[1] = u.y;
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v.w[e] = reinterpret_cast<const uint32_t*>(p)[at(e)];
+    } else {
+      const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) v.w[i] = h[at(2 * i)] | (uint32_t)h[at(2 * i + 1)] << 16;
     }
     return v;
   }
-  template <typename T>
-  __device__ __forceinline__ void store(T* p, const Vec<T, 4>& v) const {
-    if (CONTIG) {
-      if (any()) *reinterpret_cast<Vec<T, 4>*>(p + col) = v;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (has(e)) p[at(e)] = v.v[e];
-    }
-  }
 };
-
-template <typename T, typename W, bool CONTIG, int NV, bool MULTI>
-__global__ void __launch_bounds__(512) norm_fwd_kernel(const NormArgs p) {
-  __shared__ float2 red[64];
-  __shared__ uint64_t bars[kBars];
-  __shared__ uint32_t abort_word;
-  extern __shared__ __align__(16) uint8_t smem[];
-  init_bars(bars, &abort_word, p.at_once * p.slots);
-  Row<MULTI> me(p, red);
-  Ring<T, 1> ring(p, me.group, bars, smem, &abort_word);
-  const int64_t first = (int64_t)blockIdx.x * p.at_once + me.group, step = (int64_t)gridDim.x * p.at_once;
-  auto source = [&](int64_t row) {
-    const uint32_t s = p.div_rows.div((uint32_t)row), i = (uint32_t)row - s * p.rows;
-    return static_cast<const T*>(p.x) + s * p.x_batch + i * p.x_row;
-  };
-  if (me.t == 0)
-    for (int k = 0; k < p.slots && first + k * step < p.total; ++k) {
-      const T* src[1] = {source(first + k * step)};
-      ring.issue(k, src);
-    }
-  for (int64_t row = first; row < p.total; row += step, ring.next()) {
-    const uint32_t s = p.div_rows.div((uint32_t)row), i = (uint32_t)row - s * p.rows;
-    const T* x = ring.row(0, static_cast<const T*>(p.x) + s * p.x_batch + i * p.x_row);
-    const bool ok = ring.wait();       // (after one that ran out the rows' barriers are still kept)
-    Vec<T, 4> v[NV];
-#pragma unroll
-    for (int k = 0; k < NV; ++k) v[k] = Piece<CONTIG>(me.t, k, me.threads, p.C).load(x);
-    float2 sum[2] = {both(0.f), both(0.f)};
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      float2 f[2];
-      pairs<T>(v[k], f);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) sum[e & 1] = fadd2(sum[e & 1], f[e]);
-    }
-    sum[0] = fadd2(sum[0], sum[1]);
-    const float mean = me.sum(make_float2(sum[0].x + sum[0].y, 0.f), p.warps).x * p.inv_c;
-    if (me.t == 0 && ok && row + p.slots * step < p.total) {     // every thread of the row has read its slot
-      const T* src[1] = {source(row + p.slots * step)};
-      ring.issue(ring.slot, src);
-    }
-    const float2 nm = both(-mean);
-    float2 sq[2] = {both(0.f), both(0.f)};
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      opaque(v[k]);                    // convert again instead of keeping fp32 copies
-      const Piece<CONTIG> at(me.t, k, me.threads, p.C);
-      if (!at.any()) continue;
-      float2 f[2];
-      pairs<T>(v[k], f);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float2 d = fadd2(f[e], nm);
-        if (!at.has(2 * e)) d.x = 0.f;
-        if (!at.has(2 * e + 1)) d.y = 0.f;
-        sq[e & 1] = ffma2(d, d, sq[e & 1]);
-      }
-    }
-    sq[0] = fadd2(sq[0], sq[1]);
-    const float rstd = 1.0f / sqrtf(me.sum(make_float2(sq[0].x + sq[0].y, 0.f), p.warps).x * p.inv_c + p.eps);
-    if (!ok) continue;
-    T* y = static_cast<T*>(p.y) + s * p.y_batch + i * p.y_row;
-    const W* w = p.w ? static_cast<const W*>(p.w) + s * p.w_batch : nullptr;
-    const W* b = p.b ? static_cast<const W*>(p.b) + s * p.w_batch : nullptr;
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      opaque(v[k]);
-      const Piece<CONTIG> at(me.t, k, me.threads, p.C);
-      if (!at.any()) continue;
-      float2 f[2], wv[2], bv[2];
-      pairs<T>(v[k], f);
-      if (w) pairs<W>(at.load(w), wv);
-      if (b) pairs<W>(at.load(b), bv);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        f[e] = fmul2(fadd2(f[e], nm), both(rstd));
-        f[e] = ffma2(f[e], w ? fadd2(wv[e], both(p.plus)) : both(1.0f), b ? bv[e] : both(0.f));
-      }
-      unpairs<T>(v[k], f);
-      at.store(y, v[k]);
-    }
-    if (me.t == 0) {
-      if (p.mean) p.mean[row] = mean;
-      if (p.rstd) p.rstd[row] = rstd;
-    }
-  }
-  report(&abort_word);
-}
 
 // One block walks the rows [r0, r1) of run blockIdx.x, its row groups in turn.
 template <typename T, typename W, bool CONTIG, int NV, bool MULTI>
-__global__ void __launch_bounds__(512) norm_bwd_kernel(const NormArgs p) {
+__global__ void __launch_bounds__(NV == 8 ? 544 : 512) norm_fwd_kernel(const NormArgs p) {
   __shared__ float2 red[64];
   __shared__ uint64_t bars[kBars];
   __shared__ uint32_t abort_word;
   extern __shared__ __align__(16) uint8_t smem[];
-  init_bars(bars, &abort_word, p.at_once * p.slots);
+  init_bars(bars, &abort_word, 2 * p.at_once * p.slots);
+  const int first = blockIdx.x * p.at_once, r1 = (int)p.total, step = gridDim.x * p.at_once;
+  if (threadIdx.x >= p.at_once * p.warps * 32) {             // producer warp: a lane to a row group
+    const int group = threadIdx.x & 31;
+    if (group < p.at_once) {
+      Ring<T, 1> ring(p, group, bars, smem, &abort_word);
+      for (int row = first + group; row < r1; row += step, ring.next()) {
+        if (!ring.wait_free()) break;
+        const uint32_t s = p.div_rows.div(row), i = row - s * p.rows;
+        const T* src[1] = {static_cast<const T*>(p.x) + s * p.x_batch + i * p.x_row};
+        ring.issue(ring.slot, src);
+      }
+    }
+    __syncwarp();
+    report(&abort_word);
+    return;
+  }
   Row<MULTI> me(p, red);
+  const Span<CONTIG, NV> at(me.t, p.C);
+  Ring<T, 1> ring(p, me.group, bars, smem, &abort_word);
+  const int r0 = first + me.group;
+  float2 w[NV][2], b[NV][2];
+  int64_t loaded = -1;                 // whose weight these are
+  // Two rows at a time, whose sums share the shuffles and barriers: a row alone is one long chain of
+  // them.  (Rows of two samples with a weight each go one by one.)
+  for (int row = r0; row < r1;) {
+    int at_row[2] = {row, row + step};
+    uint32_t smp[2] = {p.div_rows.div(row), 0};
+    bool two = at_row[1] < r1;
+    if (two) smp[1] = p.div_rows.div(at_row[1]);
+    two = two && (p.w_batch == 0 || smp[1] == smp[0]);
+    const int64_t weight = smp[0] * p.w_batch;
+    if (weight != loaded) {
+      loaded = weight;
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        w[k][0] = w[k][1] = both(1.f);
+        b[k][0] = b[k][1] = both(0.f);
+        if (p.w) {
+          pairs<W>(at.load_any(static_cast<const W*>(p.w) + loaded, k), w[k]);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) w[k][e] = fadd2(w[k][e], both(p.plus));
+        }
+        if (p.b) pairs<W>(at.load_any(static_cast<const W*>(p.b) + loaded, k), b[k]);
+      }
+    }
+    float2 v[2][NV][2], sum[2] = {both(0.f), both(0.f)};
+    int slot[2] = {0, 0};
+    bool ok = true;                    // (after a wait that ran out the rows' barriers are still kept)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      if (r == 1 && !two) break;
+      const T* x = ring.row(0, static_cast<const T*>(p.x) + smp[r] * p.x_batch + (at_row[r] - smp[r] * p.rows) * p.x_row);
+      ok = ring.wait() && ok;
+      Raw<T> raw[NV];
+      at.load_row(x, raw);
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        pairs<T>(raw[k], v[r][k]);
+        sum[r] = fadd2(sum[r], fadd2(v[r][k][0], v[r][k][1]));
+      }
+      slot[r] = ring.slot;
+      ring.next();
+    }
+    float2 mean = me.sum(make_float2(sum[0].x + sum[0].y, sum[1].x + sum[1].y), p.warps);
+    mean = make_float2(mean.x * p.inv_c, mean.y * p.inv_c);
+    if (me.t == 0) {                   // every thread of the rows has read their slots
+      ring.release(slot[0]);
+      if (two) ring.release(slot[1]);
+    }
+    float2 sq[2] = {both(0.f), both(0.f)};
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      if (r == 1 && !two) break;
+      const float2 nm = both(r ? -mean.y : -mean.x);
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) v[r][k][e] = fadd2(v[r][k][e], nm);
+      if (!at.full) {                  // the zeros behind the row stay zeros
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            v[r][k][e].x = at.has(k, 2 * e) ? v[r][k][e].x : 0.f;
+            v[r][k][e].y = at.has(k, 2 * e + 1) ? v[r][k][e].y : 0.f;
+          }
+      }
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) sq[r] = ffma2(v[r][k][e], v[r][k][e], sq[r]);
+    }
+    const float2 var = me.sum(make_float2(sq[0].x + sq[0].y, sq[1].x + sq[1].y), p.warps);
+    const float2 rs = make_float2(1.0f / sqrtf(var.x * p.inv_c + p.eps), 1.0f / sqrtf(var.y * p.inv_c + p.eps));
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      if (!ok || (r == 1 && !two)) break;
+      const float rstd = r ? rs.y : rs.x;
+      T* y = static_cast<T*>(p.y) + smp[r] * p.y_batch + (at_row[r] - smp[r] * p.rows) * p.y_row;
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) v[r][k][e] = ffma2(fmul2(v[r][k][e], both(rstd)), w[k][e], b[k][e]);
+        Raw<T> out;
+        unpairs<T>(out, v[r][k]);
+        at.store(y, k, out);
+      }
+      if (me.t == 0) {
+        if (p.mean) p.mean[at_row[r]] = r ? mean.y : mean.x;
+        if (p.rstd) p.rstd[at_row[r]] = rstd;
+      }
+    }
+    row += two ? 2 * step : step;
+  }
+}
+
+// The forward pass of rows of more than 512 contiguous 16-bit elements, up to 2,048: a warp to a row, so
+// that no barrier joins its sums, two rows at a time.  A lane keeps its elements as they were read (64 at
+// most) and converts them for each of the three passes; the weight and bias, too many for registers,
+// come from L1, once for both rows.
+template <typename T, typename W, int NV>
+__global__ void __launch_bounds__(512) norm_wide_kernel(const NormArgs p) {
+  __shared__ uint64_t bars[kBars];
+  __shared__ uint32_t abort_word;
+  extern __shared__ __align__(16) uint8_t smem[];
+  init_bars(bars, &abort_word, 2 * p.at_once * p.slots);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int first = blockIdx.x * p.at_once, r1 = (int)p.total, step = gridDim.x * p.at_once;
+  if (warp == p.at_once) {             // producer warp: a lane to a row group
+    if (lane < p.at_once) {
+      Ring<T, 1> ring(p, lane, bars, smem, &abort_word);
+      for (int row = first + lane; row < r1; row += step, ring.next()) {
+        if (!ring.wait_free()) break;
+        const uint32_t s = p.div_rows.div(row), i = row - s * p.rows;
+        const T* src[1] = {static_cast<const T*>(p.x) + s * p.x_batch + i * p.x_row};
+        ring.issue(ring.slot, src);
+      }
+    }
+    __syncwarp();
+    report(&abort_word);
+    return;
+  }
+  Ring<T, 1> ring(p, warp, bars, smem, &abort_word);
+  const Span<true, NV> at(lane, p.C);
+  const float2 plus = both(p.w ? p.plus : 1.f);
+  for (int row = first + warp; row < r1;) {
+    uint32_t smp[2] = {p.div_rows.div(row), 0};
+    bool two = row + step < r1;
+    if (two) smp[1] = p.div_rows.div(row + step);
+    two = two && (p.w_batch == 0 || smp[1] == smp[0]);
+    Raw<T> v[2][NV];
+    float2 sum[2] = {both(0.f), both(0.f)};
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      if (r == 1 && !two) break;
+      const int i = row + r * step - smp[r] * p.rows;
+      if (!ring.wait()) return;
+      at.load_row(ring.row(0, static_cast<const T*>(p.x) + smp[r] * p.x_batch + i * p.x_row), v[r]);
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        float2 f[2];
+        pairs<T>(v[r][k], f);
+        sum[r] = fadd2(sum[r], fadd2(f[0], f[1]));
+      }
+      __syncwarp();
+      if (lane == 0) ring.release(ring.slot);
+      ring.next();
+    }
+    float mean[2], rstd[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) mean[r] = warp_sum(sum[r].x + sum[r].y) * p.inv_c;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const float2 nm = both(-mean[r]);
+      float2 sq = both(0.f);
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        opaque(v[r][k]);               // convert again instead of keeping fp32 copies
+        float2 f[2];
+        pairs<T>(v[r][k], f);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float2 d = fadd2(f[e], nm);
+          if (!at.full && !at.has(k, 0)) d = both(0.f);      // the zeros behind the row stay zeros
+          sq = ffma2(d, d, sq);
+        }
+      }
+      rstd[r] = sq.x + sq.y;
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) rstd[r] = 1.0f / sqrtf(warp_sum(rstd[r]) * p.inv_c + p.eps);
+    const W* w = static_cast<const W*>(p.w) + smp[0] * p.w_batch;
+    const W* b = static_cast<const W*>(p.b) + smp[0] * p.w_batch;
+    T* y[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) y[r] = static_cast<T*>(p.y) + smp[r] * p.y_batch + (int64_t)(row + r * step - smp[r] * p.rows) * p.y_row;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      float2 wv[2] = {both(0.f), both(0.f)}, bv[2] = {both(0.f), both(0.f)};
+      if (p.w) pairs<W>(at.load_any(w, k), wv);
+      if (p.b) pairs<W>(at.load_any(b, k), bv);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        if (r == 1 && !two) break;
+        opaque(v[r][k]);
+        float2 f[2];
+        pairs<T>(v[r][k], f);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          f[e] = ffma2(fmul2(fadd2(f[e], both(-mean[r])), both(rstd[r])), fadd2(wv[e], plus), bv[e]);
+        Raw<T> out;
+        unpairs<T>(out, f);
+        at.store(y[r], k, out);
+      }
+    }
+    if (lane < (two ? 2 : 1)) {
+      if (p.mean) p.mean[row + lane * step] = lane ? mean[1] : mean[0];
+      if (p.rstd) p.rstd[row + lane * step] = lane ? rstd[1] : rstd[0];
+    }
+    row += two ? 2 * step : step;
+  }
+}
+
+// The same walk; the columns' sums of dy xh and dy stay in registers.
+template <typename T, typename W, bool CONTIG, int NV, bool MULTI>
+__global__ void __launch_bounds__(NV == 8 ? 544 : 512) norm_bwd_kernel(const NormArgs p) {
+  __shared__ float2 red[64];
+  __shared__ uint64_t bars[kBars];
+  __shared__ uint32_t abort_word;
+  extern __shared__ __align__(16) uint8_t smem[];
+  init_bars(bars, &abort_word, 2 * p.at_once * p.slots);
+  const int64_t group = blockIdx.x / p.runs_per_group, run = blockIdx.x - group * p.runs_per_group;
+  const int first = (int)(group * p.group_rows + p.group_rows * run / p.runs_per_group);
+  const int r1 = (int)(group * p.group_rows + p.group_rows * (run + 1) / p.runs_per_group);
+  if (threadIdx.x >= p.at_once * p.warps * 32) {             // producer warp: a lane to a row group
+    const int g = threadIdx.x & 31;
+    if (g < p.at_once) {
+      Ring<T, 2> ring(p, g, bars, smem, &abort_word);
+      for (int row = first + g; row < r1; row += p.at_once, ring.next()) {
+        if (!ring.wait_free()) break;
+        const uint32_t s = p.div_rows.div(row), i = row - s * p.rows;
+        const T* src[2] = {static_cast<const T*>(p.x) + s * p.x_batch + i * p.x_row,
+                           static_cast<const T*>(p.dy) + s * p.dy_batch + i * p.dy_row};
+        ring.issue(ring.slot, src);
+      }
+    }
+    __syncwarp();
+    report(&abort_word);
+    if (p.part) {                      // the barriers of the sums below
+      __syncthreads();
+      if (p.at_once > 1) __syncthreads();
+    }
+    return;
+  }
+  Row<MULTI> me(p, red);
+  const Span<CONTIG, NV> at(me.t, p.C);
   Ring<T, 2> ring(p, me.group, bars, smem, &abort_word);
-  const int64_t group = blockIdx.x / p.runs_per_group;
-  const int64_t run = blockIdx.x - group * p.runs_per_group;
-  const int64_t r0 = group * p.group_rows + p.group_rows * run / p.runs_per_group;
-  const int64_t r1 = group * p.group_rows + p.group_rows * (run + 1) / p.runs_per_group;
-  float2 dw[NV][2], db[NV][2];
+  const int r0 = first + me.group;
+  float2 dw[NV][2], db[NV][2], w[NV][2];
 #pragma unroll
   for (int k = 0; k < NV; ++k)
 #pragma unroll
-    for (int e = 0; e < 2; ++e) dw[k][e] = db[k][e] = both(0.f);
-  auto issue = [&](int slot, int64_t row) {
-    const uint32_t s = p.div_rows.div((uint32_t)row), i = (uint32_t)row - s * p.rows;
-    const T* src[2] = {static_cast<const T*>(p.x) + s * p.x_batch + i * p.x_row,
-                       static_cast<const T*>(p.dy) + s * p.dy_batch + i * p.dy_row};
-    ring.issue(slot, src);
-  };
-  if (me.t == 0)
-    for (int k = 0; k < p.slots && r0 + me.group + k * p.at_once < r1; ++k) issue(k, r0 + me.group + k * p.at_once);
-  float mean = 0.f, rstd = 0.f;        // of the next row
-  if (r0 + me.group < r1) {
-    mean = __ldg(p.mean + r0 + me.group);
-    rstd = __ldg(p.rstd + r0 + me.group);
+    for (int e = 0; e < 2; ++e) {
+      dw[k][e] = db[k][e] = both(0.f);
+      w[k][e] = both(1.f);
+    }
+  if (p.w) {                           // a run's rows share their weight
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      pairs<W>(at.load_any(static_cast<const W*>(p.w) + group * p.w_batch, k), w[k]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) w[k][e] = fadd2(w[k][e], both(p.plus));
+    }
   }
-  for (int64_t row = r0 + me.group; row < r1; row += p.at_once, ring.next()) {
-    const uint32_t s = p.div_rows.div((uint32_t)row), i = (uint32_t)row - s * p.rows;
+  float mean = 0.f, rstd = 0.f;        // of the next row
+  if (r0 < r1) {
+    mean = __ldg(p.mean + r0);
+    rstd = __ldg(p.rstd + r0);
+  }
+  for (int row = r0; row < r1; row += p.at_once, ring.next()) {
+    const uint32_t s = p.div_rows.div(row), i = row - s * p.rows;
     const T* x = ring.row(0, static_cast<const T*>(p.x) + s * p.x_batch + i * p.x_row);
     const T* dy = ring.row(1, static_cast<const T*>(p.dy) + s * p.dy_batch + i * p.dy_row);
-    const W* w = p.w ? static_cast<const W*>(p.w) + s * p.w_batch : nullptr;
-    const float2 nm = both(-mean), rs = both(rstd), plus = both(p.plus);
+    const float2 nm = both(-mean), rs = both(rstd);
     if (row + p.at_once < r1) {
       mean = __ldg(p.mean + row + p.at_once);
       rstd = __ldg(p.rstd + row + p.at_once);
     }
     const bool ok = ring.wait();       // (after one that ran out the rows' barriers are still kept)
-    Vec<T, 4> xv[NV], gv[NV];
+    float2 xh[NV][2], g[NV][2], a = both(0.f), b = both(0.f);
+    Raw<T> rx[NV], rg[NV];
+    at.load_row(x, rx);
+    at.load_row(dy, rg);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const Piece<CONTIG> at(me.t, k, me.threads, p.C);
-      xv[k] = at.load(x);
-      gv[k] = at.load(dy);
-    }
-    float2 a = both(0.f), b = both(0.f);
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const Piece<CONTIG> at(me.t, k, me.threads, p.C);
-      if (!at.any()) continue;
-      float2 xf[2], gf[2], wv[2];
-      pairs<T>(xv[k], xf);
-      pairs<T>(gv[k], gf);
-      if (w) pairs<W>(at.load(w), wv);
+      pairs<T>(rx[k], xh[k]);
+      pairs<T>(rg[k], g[k]);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float2 xh = fmul2(fadd2(xf[e], nm), rs);
-        dw[k][e] = ffma2(gf[e], xh, dw[k][e]);
-        db[k][e] = fadd2(db[k][e], gf[e]);
-        const float2 g = w ? fmul2(gf[e], fadd2(wv[e], plus)) : gf[e];
-        a = fadd2(a, g);
-        b = ffma2(g, xh, b);
+        xh[k][e] = fmul2(fadd2(xh[k][e], nm), rs);
+        dw[k][e] = ffma2(g[k][e], xh[k][e], dw[k][e]);
+        db[k][e] = fadd2(db[k][e], g[k][e]);
+        g[k][e] = fmul2(g[k][e], w[k][e]);
+        a = fadd2(a, g[k][e]);
+        b = ffma2(g[k][e], xh[k][e], b);
       }
     }
     const float2 ab = me.sum(make_float2(a.x + a.y, b.x + b.y), p.warps);
-    if (me.t == 0 && ok && row + (int64_t)p.slots * p.at_once < r1) issue(ring.slot, row + (int64_t)p.slots * p.at_once);
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {     // convert again below instead of keeping fp32 copies
-      opaque(xv[k]);
-      opaque(gv[k]);
-    }
-    const float2 am = both(-ab.x * p.inv_c), bm = both(-ab.y * p.inv_c);
+    if (me.t == 0) ring.release(ring.slot);     // every thread of the row has read its slot
     if (!ok) continue;
+    const float2 am = both(-ab.x * p.inv_c), bm = both(-ab.y * p.inv_c);
     T* dx = static_cast<T*>(p.y) + s * p.y_batch + i * p.y_row;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const Piece<CONTIG> at(me.t, k, me.threads, p.C);
-      if (!at.any()) continue;
-      float2 xf[2], gf[2], wv[2];
-      pairs<T>(xv[k], xf);
-      pairs<T>(gv[k], gf);
-      if (w) pairs<W>(at.load(w), wv);       // (again: cheaper than keeping g in fp32)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float2 xh = fmul2(fadd2(xf[e], nm), rs);
-        const float2 g = w ? fmul2(gf[e], fadd2(wv[e], plus)) : gf[e];
-        xf[e] = fmul2(rs, ffma2(xh, bm, fadd2(g, am)));
-      }
-      unpairs<T>(gv[k], xf);
-      at.store(dx, gv[k]);
+      for (int e = 0; e < 2; ++e) g[k][e] = fmul2(rs, ffma2(xh[k][e], bm, fadd2(g[k][e], am)));
+      Raw<T> out;
+      unpairs<T>(out, g[k]);
+      at.store(dx, k, out);
     }
   }
-  report(&abort_word);
   if (!p.part) return;
   // the row groups hold sums of the same columns: side by side in the slots' memory, then added in order
   float* out = p.part + (int64_t)blockIdx.x * 2 * p.C;
@@ -418,18 +623,17 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormArgs p) {
   float* mine = p.at_once > 1 ? acc + (int64_t)me.group * 2 * p.C : out;
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const Piece<CONTIG> at(me.t, k, me.threads, p.C);
+  for (int k = 0; k < NV; ++k)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      if (at.at(e) >= p.C) continue;
-      mine[at.at(e)] = e & 1 ? dw[k][e / 2].y : dw[k][e / 2].x;
-      mine[p.C + at.at(e)] = e & 1 ? db[k][e / 2].y : db[k][e / 2].x;
+      if (!at.has(k, e)) continue;
+      const int c = at.col + at.offset(k, e);
+      mine[c] = e & 1 ? dw[k][e / 2].y : dw[k][e / 2].x;
+      mine[p.C + c] = e & 1 ? db[k][e / 2].y : db[k][e / 2].x;
     }
-  }
   if (p.at_once == 1) return;
   __syncthreads();
-  for (int c = threadIdx.x; c < 2 * p.C; c += blockDim.x) {
+  for (int c = threadIdx.x; c < 2 * p.C; c += blockDim.x - 32) {
     float t = acc[c];
     for (int q = 1; q < p.at_once; ++q) t += acc[(int64_t)q * 2 * p.C + c];
     out[c] = t;
@@ -455,36 +659,35 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* part, in
   if (threadIdx.x == 0 && col < C) out[g * C + col] = from_f32<O>(s);
 }
 
-// How a row is spread: its warps and its pieces of four elements per lane, at most 16 of 16 bits and 8 of
-// 32 bits or not contiguous; in the backward pass, with two sums beside each element, 6 and 4.  The
-// widest rows take 8, so that 16 warps hold them.
+// How a row is spread: its warps, and its pieces of four elements per lane, four at most (eight where 15
+// warps would not hold the row).
 struct Spread {
   int warps, nv;
 };
-Spread spread(bool bwd, bool contig, int C, int elem) {
-  const bool light = contig && elem == 2;
-  const int most = !bwd ? (light ? 16 : 8) : (C <= 8192 ? (light ? 6 : 4) : 8);
-  const int pieces = (C + 3) / 4;
+Spread spread(int C) {
+  const int most = C <= 7680 ? 4 : 8, pieces = (C + 3) / 4;
   const int warps = (pieces + 32 * most - 1) / (32 * most);
   return {warps, (pieces + 32 * warps - 1) / (32 * warps)};
 }
 
-constexpr int kSmem = 200 * 1024;      // dynamic shared memory of a block at most
+constexpr int kSmem = 200 * 1024;      // shared memory for the slots of a block at most
+constexpr int kSlack = 4096;           // the row's last warp reads its whole span, up to 1,024 elements
 
-// Rows of a block at a time (16 warps, one block per multiprocessor; named barriers give 15 groups of
-// warps), and the rows in flight behind each: as many as fit, 8 at most.  The backward pass's groups
+// Rows of a block at a time (15 warps and the producer, one block per multiprocessor: 512 threads leave
+// 128 registers to each), and the rows in flight behind each: as many as fit, 8 at most.  The backward pass's groups
 // leave their sums in the same memory.
 void plan_block(NormArgs& a, bool bwd, int elem, int64_t rows_per_block) {
   const int tensors = bwd ? 2 : 1;
   a.slot_bytes = (a.C * elem + 31) & ~15;                  // a row that starts anywhere
-  a.at_once = a.warps > 1 ? std::min(15, 16 / a.warps) : 16;
+  a.at_once = std::max(1, 15 / a.warps);                   // (the widest rows: 16 warps and the producer)
   a.at_once = (int)std::max<int64_t>(1, std::min<int64_t>(a.at_once, rows_per_block));
   a.at_once = std::min(a.at_once, std::max(1, kSmem / (tensors * a.slot_bytes)));
   if (bwd) a.at_once = std::min(a.at_once, std::max(1, kSmem / (2 * a.C * (int)sizeof(float))));
-  a.slots = std::max(1, std::min(8, kSmem / (a.at_once * tensors * a.slot_bytes)));
+  // (a wide row's weight needs room in L1)
+  a.slots = std::max(1, std::min(a.wide ? 2 : 8, kSmem / (a.at_once * tensors * a.slot_bytes)));
 }
 int smem_bytes(const NormArgs& a, bool bwd) {
-  const int ring = a.at_once * a.slots * (bwd ? 2 : 1) * a.slot_bytes;
+  const int ring = a.at_once * a.slots * (bwd ? 2 : 1) * a.slot_bytes + kSlack;
   return std::max(ring, bwd && a.at_once > 1 ? a.at_once * 2 * a.C * (int)sizeof(float) : 0);
 }
 
@@ -503,30 +706,37 @@ cudaError_t launch_one(K kernel, int blocks, int threads, int smem, const NormAr
   return cudaGetLastError();
 }
 
+template <typename T, typename W>
+cudaError_t launch_wide(const NormArgs& a, int blocks, cudaStream_t st) {
+  const int threads = 32 * (a.at_once + 1), smem = smem_bytes(a, false);
+  if (a.C <= 1024) return launch_one(norm_wide_kernel<T, W, 8>, blocks, threads, smem, a, st);
+  if (a.C <= 1536) return launch_one(norm_wide_kernel<T, W, 12>, blocks, threads, smem, a, st);
+  return launch_one(norm_wide_kernel<T, W, 16>, blocks, threads, smem, a, st);
+}
+
 template <typename T, typename W, bool CONTIG, int NV>
 cudaError_t launch_nv(bool bwd, const NormArgs& a, int blocks, cudaStream_t st) {
-  const int threads = 32 * a.warps * a.at_once, smem = smem_bytes(a, bwd);
+  const int threads = 32 * (a.warps * a.at_once + 1), smem = smem_bytes(a, bwd);
   if (!bwd)
     return a.warps > 1 ? launch_one(norm_fwd_kernel<T, W, CONTIG, NV, true>, blocks, threads, smem, a, st)
                        : launch_one(norm_fwd_kernel<T, W, CONTIG, NV, false>, blocks, threads, smem, a, st);
-  if constexpr (NV <= 8)                                   // (no more: see spread)
-    return a.warps > 1 ? launch_one(norm_bwd_kernel<T, W, CONTIG, NV, true>, blocks, threads, smem, a, st)
-                       : launch_one(norm_bwd_kernel<T, W, CONTIG, NV, false>, blocks, threads, smem, a, st);
-  return cudaErrorInvalidValue;
+  return a.warps > 1 ? launch_one(norm_bwd_kernel<T, W, CONTIG, NV, true>, blocks, threads, smem, a, st)
+                     : launch_one(norm_bwd_kernel<T, W, CONTIG, NV, false>, blocks, threads, smem, a, st);
 }
 
 template <typename T, typename W, bool CONTIG>
 cudaError_t launch_pieces(bool bwd, const NormArgs& a, int nv, int blocks, cudaStream_t st) {
-  return nv <= 2    ? launch_nv<T, W, CONTIG, 2>(bwd, a, blocks, st)
-         : nv <= 4  ? launch_nv<T, W, CONTIG, 4>(bwd, a, blocks, st)
-         : nv <= 6  ? launch_nv<T, W, CONTIG, 6>(bwd, a, blocks, st)
-         : nv <= 8  ? launch_nv<T, W, CONTIG, 8>(bwd, a, blocks, st)
-         : nv <= 12 ? launch_nv<T, W, CONTIG, 12>(bwd, a, blocks, st)
-                    : launch_nv<T, W, CONTIG, 16>(bwd, a, blocks, st);
+  return nv <= 1   ? launch_nv<T, W, CONTIG, 1>(bwd, a, blocks, st)
+         : nv <= 2 ? launch_nv<T, W, CONTIG, 2>(bwd, a, blocks, st)
+         : nv <= 3 ? launch_nv<T, W, CONTIG, 3>(bwd, a, blocks, st)
+         : nv <= 4 ? launch_nv<T, W, CONTIG, 4>(bwd, a, blocks, st)
+                   : launch_nv<T, W, CONTIG, 8>(bwd, a, blocks, st);
 }
 
 template <typename T, typename W>
 cudaError_t launch_norm(bool bwd, bool contig, const NormArgs& a, int nv, int blocks, cudaStream_t st) {
+  if constexpr (sizeof(T) == 2)
+    if (a.wide) return launch_wide<T, W>(a, blocks, st);
   return contig ? launch_pieces<T, W, true>(bwd, a, nv, blocks, st) : launch_pieces<T, W, false>(bwd, a, nv, blocks, st);
 }
 
@@ -619,7 +829,10 @@ int ultragen_layer_norm(const ultragen_norm_t* n, const void* x, const void* wei
   a.mean = mean;
   a.rstd = rstd;
   const bool contig = contiguous_pieces(n, x, nullptr, y, weight, bias);
-  const Spread sp = spread(false, contig, n->cols, elem_size(n->dtype));
+  Spread sp = spread(n->cols);
+  // Enough rows to give every warp some: with fewer the row groups' warps share a row's work.
+  a.wide = contig && n->dtype != ULTRAGEN_F32 && n->cols > 512 && n->cols <= 2048 && a.total >= 32 * (int64_t)sm_count();
+  if (a.wide) sp.warps = 1;
   a.warps = sp.warps;
   plan_block(a, false, elem_size(n->dtype), (a.total + sm_count() - 1) / sm_count());
   const int64_t blocks = std::min<int64_t>((a.total + a.at_once - 1) / a.at_once, sm_count());
@@ -659,7 +872,7 @@ int ultragen_layer_norm_backward(const ultragen_norm_t* n, const void* dy, const
   if (!dy || !x || !mean || !rstd || !dx) return ULTRAGEN_ERR_INVALID_ARG;
   if ((st = current_device(&dev)) != ULTRAGEN_OK) return st;
   const bool contig = contiguous_pieces(n, x, dy, dx, weight, nullptr);
-  const Spread sp = spread(true, contig, n->cols, elem_size(n->dtype));
+  const Spread sp = spread(n->cols);
   a.warps = sp.warps;
   a.runs_per_group = runs_of(a.group_rows, groups, sm_count());
   plan_block(a, true, elem_size(n->dtype), (a.group_rows + a.runs_per_group - 1) / a.runs_per_group);
