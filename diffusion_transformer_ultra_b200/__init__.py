@@ -8,7 +8,7 @@ from ._ffi import (BF16, F16, F32, QK_BF16, QK_E4M3, HostRunner, Layer, Plan, Ul
                    hla_forward,
                    hla_forward_noalloc, hla_forward_raster, lib, permute_rope,
                    unpermute, warm_start)
-from .around import (adapter_project, cross_attention, cross_attention_backward,  # noqa: F401
+from .around import (ProjectedLayer, adapter_project, cross_attention, cross_attention_backward,  # noqa: F401
                      layer_norm, layer_norm_backward, operator_status)
 from .inputs import (WARM_WORKLOADS, WORKLOADS, WarmWorkload, Workload,  # noqa: F401
                      make_qkv, make_warm)

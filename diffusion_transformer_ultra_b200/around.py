@@ -307,3 +307,43 @@ def cross_attention_backward(do, q, k, v, o, lse, dq, dk, dv, kv_lens=None, key_
             _ptr(kv_lens), _ptr(key_mask), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(ws),
             ws.numel() if ws is not None else 0, _stream(q.device)))
     return dq, dk, dv
+
+
+# ------------------------------------------------------------------------------- layers
+class ProjectedLayer:
+    """One attention layer from hidden states: layer norm (modulated per sample), the Q, K and V
+    projections with each token's adapter beside them, the joint attention of `Layer`, and, where
+    states are given, cross attention of the normed tokens' queries to an encoder's states.  The
+    buffers stay resident between calls; every step runs on `stream`."""
+
+    def __init__(self, plan, batch: int, channels: int, device="cuda"):
+        i = plan.info
+        self.layer = _ffi.Layer(plan, batch, device)
+        self.shape = (batch, i["N_raster"], i["heads"], i["head_dim"])
+        self.norm = torch.empty((batch, i["N_raster"], channels), dtype=torch.bfloat16, device=device)
+        self.q, self.k, self.v, self.xq = (torch.empty(self.shape, dtype=torch.bfloat16, device=device)
+                                           for _ in range(4))
+
+    def project(self, w, out, a, b, ids, scales=None, bias=None, stream=None):
+        """out [batch, N_raster, heads, head_dim] = the projection of the normed tokens."""
+        B, N, H, D = self.shape
+        adapter_project(self.norm.view(B * N, -1), w, out.view(B * N, H * D), a, b, ids, scales=scales,
+                        bias=bias, stream=stream)
+        return out
+
+    def __call__(self, x, o, w, a, b, ids, scales=None, bias=None, weight=None, shift=None, eps: float = 1e-6,
+                 plus_one: bool = True, stream=None):
+        """x [batch, N_raster, channels] bf16, o [batch, N_raster, heads, head_dim]; w, a, b (and bias)
+        are triples for Q, K and V as adapter_project takes them; ids [batch * N_raster]; weight and
+        shift are the norm's weight and bias."""
+        layer_norm(x, self.norm, weight, shift, eps=eps, plus_one=plus_one, stream=stream)
+        for i, out in enumerate((self.q, self.k, self.v)):
+            self.project(w[i], out, a[i], b[i], ids, scales, None if bias is None else bias[i], stream)
+        return self.layer(self.q, self.k, self.v, o, stream)
+
+    def cross(self, o, w, a, b, ids, k, v, scales=None, bias=None, kv_lens=None, key_mask=None, lse=None,
+              stream=None):
+        """o = cross attention of the tokens normed by the last call, projected by w, to the states'
+        keys and values k, v [batch, ns, kv_heads, head_dim]."""
+        self.project(w, self.xq, a, b, ids, scales, bias, stream)
+        return cross_attention(self.xq, k, v, o, kv_lens=kv_lens, key_mask=key_mask, lse=lse, stream=stream)

@@ -1,0 +1,158 @@
+"""Argument checks of the operators around the attention, without a GPU: every refusal comes before
+any pointer is used."""
+import ctypes
+import math
+
+import pytest
+
+OK, INVALID, UNSUPPORTED = 0, 1, 2
+
+
+@pytest.fixture(scope="module")
+def ffi():
+    from diffusion_transformer_ultra_b200 import _ffi, build
+    build.build()
+    return _ffi
+
+
+@pytest.fixture()
+def mem():
+    buf = ctypes.create_string_buffer(1 << 12)
+    return ctypes.addressof(buf) + (-ctypes.addressof(buf)) % 16, buf
+
+
+def norm(ffi, **kw):
+    n = dict(batch=2, rows=3, cols=64, dtype=0, wdtype=0, per_sample=0, plus_one=0, eps=1e-6, x_row=64, x_batch=192, y_row=64,
+             y_batch=192, dy_row=64, dy_batch=192)
+    n.update(kw)
+    return ffi.NormSizes(**n)
+
+
+def adapter(ffi, **kw):
+    c = dict(rows=4, k=64, n=32, rank=8, adapters=2, dtype=0, x_row=64, y_row=32)
+    c.update(kw)
+    return ffi.AdapterSizes(**c)
+
+
+def cross(ffi, **kw):
+    c = dict(batch=2, nq=5, ns=7, heads=4, kv_heads=2, head_dim=64, dtype=0, masked=0, scale=0.125)
+    c.update(kw)
+    s = ffi.CrossSizes(**c)
+    for t in range(8):
+        s.stride[t][:] = (1 << 12, 256, 64)
+    return s
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(batch=-1), INVALID), (dict(rows=-1), INVALID), (dict(cols=0), INVALID), (dict(dtype=9), INVALID),
+    (dict(wdtype=2), INVALID), (dict(eps=-1.0), INVALID), (dict(eps=math.nan), INVALID), (dict(eps=math.inf), INVALID),
+    (dict(cols=16385), UNSUPPORTED), (dict(batch=1 << 16, rows=1 << 16), UNSUPPORTED),
+    (dict(batch=1 << 16, per_sample=1), UNSUPPORTED)])
+def test_layer_norm_sizes(ffi, mem, bad, status):
+    a, _ = mem
+    L, n, need = ffi.lib(), norm(ffi, **bad), ctypes.c_size_t()
+    assert L.ultragen_layer_norm(n, a, None, None, a, None, None, None) == status
+    assert L.ultragen_layer_norm_backward_workspace(n, ctypes.byref(need)) == status
+    assert L.ultragen_layer_norm_backward(n, a, a, None, a, a, a, None, None, 0, None, 0, None) == status
+
+
+def test_layer_norm_pointers(ffi, mem):
+    a, _ = mem
+    L, n, need = ffi.lib(), norm(ffi), ctypes.c_size_t()
+    assert L.ultragen_layer_norm(n, None, None, None, a, None, None, None) == INVALID
+    assert L.ultragen_layer_norm(n, a, None, None, None, None, None, None) == INVALID
+    assert L.ultragen_layer_norm(None, a, None, None, a, None, None, None) == INVALID
+    assert L.ultragen_layer_norm(norm(ffi, rows=0), None, None, None, None, None, None, None) == OK
+    for hole in range(5):
+        p = [a] * 5
+        p[hole] = None
+        assert L.ultragen_layer_norm_backward(n, p[0], p[1], None, p[2], p[3], p[4], None, None, 0, None, 0, None) == INVALID
+    assert L.ultragen_layer_norm_backward(n, a, a, None, a, a, a, None, None, 7, None, 0, None) == INVALID
+    assert L.ultragen_layer_norm_backward_workspace(n, None) == INVALID
+    assert L.ultragen_layer_norm_backward_workspace(n, ctypes.byref(need)) == OK and need.value % 16 == 0 and need.value > 0
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(rows=-1), INVALID), (dict(k=0), INVALID), (dict(n=0), INVALID), (dict(rank=0), INVALID), (dict(adapters=0), INVALID),
+    (dict(dtype=5), INVALID), (dict(rank=129), UNSUPPORTED), (dict(n=4194241), UNSUPPORTED)])
+def test_adapter_sizes(ffi, mem, bad, status):
+    a, _ = mem
+    L, c, need = ffi.lib(), adapter(ffi, **bad), ctypes.c_size_t()
+    assert L.ultragen_adapter_project_workspace(c, ctypes.byref(need)) == status
+    assert L.ultragen_adapter_project(c, a, a, None, a, a, None, a, a, a, 1 << 20, None) == status
+
+
+def test_adapter_pointers(ffi, mem):
+    a, _ = mem
+    L, c, need = ffi.lib(), adapter(ffi), ctypes.c_size_t()
+    assert L.ultragen_adapter_project_workspace(c, ctypes.byref(need)) == OK
+    order = ("x", "w", "a", "b", "ids", "y", "ws")
+
+    def call(**p):
+        q = dict.fromkeys(order, a)
+        size = p.pop("size", need.value)
+        q.update(p)
+        return L.ultragen_adapter_project(c, q["x"], q["w"], None, q["a"], q["b"], None, q["ids"], q["y"], q["ws"], size, None)
+    for name in order:
+        assert call(**{name: None}) == INVALID
+    assert call(size=need.value - 1) == INVALID
+    assert call(ws=a + 8) == INVALID
+    assert L.ultragen_adapter_project(adapter(ffi, rows=0), *[None] * 9, 0, None) == OK
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(batch=-1), INVALID), (dict(nq=-1), INVALID), (dict(ns=-1), INVALID), (dict(heads=0), INVALID), (dict(kv_heads=0), INVALID),
+    (dict(heads=3), INVALID), (dict(scale=math.nan), INVALID), (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID),
+    (dict(dtype=1), UNSUPPORTED), (dict(head_dim=96), UNSUPPORTED), (dict(heads=258, kv_heads=2), UNSUPPORTED),
+    (dict(batch=1 << 15, nq=1 << 14), UNSUPPORTED)])
+def test_cross_sizes(ffi, mem, bad, status):
+    a, _ = mem
+    L, c, need = ffi.lib(), cross(ffi, **bad), ctypes.c_size_t()
+    for back in (0, 1):
+        assert L.ultragen_cross_attention_workspace(c, back, ctypes.byref(need)) == status
+    assert L.ultragen_cross_attention(c, a, a, a, None, None, a, None, a, 1 << 20, None) == status
+    assert L.ultragen_cross_attention_backward(c, a, a, a, a, a, a, None, None, a, a, a, a, 1 << 20, None) == status
+
+
+def test_cross_pointers_and_strides(ffi, mem):
+    a, _ = mem
+    L, need = ffi.lib(), ctypes.c_size_t()
+    c = cross(ffi, masked=1)
+    assert L.ultragen_cross_attention_workspace(c, 0, ctypes.byref(need)) == OK and need.value > 0
+    assert L.ultragen_cross_attention_workspace(c, 2, ctypes.byref(need)) == INVALID
+    assert L.ultragen_cross_attention_workspace(c, 0, None) == INVALID
+    assert L.ultragen_cross_attention_workspace(c, 0, ctypes.byref(need)) == OK
+    assert L.ultragen_cross_attention(c, a, a, a, None, a, a, None, a, need.value - 1, None) == INVALID
+    assert L.ultragen_cross_attention(c, a, a, a, None, a, a, None, None, need.value, None) == INVALID
+    for hole in range(4):
+        p = [a] * 4
+        p[hole] = None
+        assert L.ultragen_cross_attention(c, *p[:3], None, a, p[3], None, a, need.value, None) == INVALID
+        p[hole] = a + 8
+        assert L.ultragen_cross_attention(c, *p[:3], None, a, p[3], None, a, need.value, None) == INVALID
+    # a mask the workspace was not sized for
+    assert L.ultragen_cross_attention(cross(ffi), a, a, a, None, a, a, None, a, 1 << 20, None) == INVALID
+    for t in range(8):
+        c = cross(ffi)
+        c.stride[t][1] = 60
+        if t < 4:
+            assert L.ultragen_cross_attention(c, a, a, a, None, None, a, None, a, 1 << 20, None) == INVALID
+        assert L.ultragen_cross_attention_backward(c, a, a, a, a, a, a, None, None, a, a, a, a, 1 << 20, None) == INVALID
+    assert L.ultragen_cross_attention(cross(ffi, batch=0), *[None] * 8, 0, None) == OK
+
+
+def test_binding_refuses_host_tensors():
+    import torch
+    import diffusion_transformer_ultra_b200 as ug
+    x = torch.zeros(2, 64)
+    with pytest.raises(ValueError, match="CUDA"):
+        ug.layer_norm(x, x)
+    with pytest.raises(ValueError, match="CUDA"):
+        ug.layer_norm_backward(x, x, x, x, x)
+    with pytest.raises(ValueError, match="CUDA"):
+        ug.adapter_project(x, x, x, x, x, x)
+    q = torch.zeros(1, 2, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        ug.cross_attention(q, q, q, q)
+    with pytest.raises(ValueError, match="CUDA"):
+        ug.cross_attention_backward(q, q, q, q, q, q, q, q, q)
