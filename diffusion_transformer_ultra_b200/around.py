@@ -20,7 +20,7 @@ _INT32_MAX = 2 ** 31 - 1
 
 
 def _tensor(t, name, dtypes, shape=None, device=None):
-    """Checks one tensor argument; dimensions of `shape` that are None may have any size."""
+    """Checks one tensor argument."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if device is not None and t.device != device:
@@ -32,6 +32,9 @@ def _tensor(t, name, dtypes, shape=None, device=None):
 
 
 def _contiguous(t, name, dtypes, shape, device):
+    # (one look at everything first: the messages cost only a call that is refused)
+    if isinstance(t, torch.Tensor) and t.device == device and t.dtype in dtypes and t.shape == shape and t.is_contiguous():
+        return
     _tensor(t, name, dtypes, shape, device)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")

@@ -123,10 +123,8 @@ __device__ __forceinline__ uint4 piece(const void* row, int64_t k, bool on) {
 }
 
 constexpr int kShrinkRows = 32;        // rows of a block of the shrink kernel
-constexpr int kGroup = 8;              // 8-column tiles of a pass over K
 
-// t = s A x of 32 rows: their distinct adapters' rows of A, 8 to a tile, up to 8 tiles a pass over
-// K.  The block's 8 warps take every eighth 32-element piece of K, so that few rows still bring
+// t = s A x of 32 rows: their distinct adapters' rows of A, 8 to a tile, NT tiles a pass over K.  The block's 8 warps take every eighth 32-element piece of K, so that few rows still bring
 // enough loads into flight; their sums meet in shared memory, in warp order.  Bound by x's bytes.
 template <typename T, int NT>
 __device__ __forceinline__ void shrink_pass(const AdapterArgs& p, const int* ids, int tile0, int ntiles, float* red) {
@@ -145,7 +143,7 @@ __device__ __forceinline__ void shrink_pass(const AdapterArgs& p, const int* ids
     a[i] = i < ntiles && r < p.R ? static_cast<const T*>(p.a) + ((int64_t)ids[q / per] * p.R + r) * p.K : nullptr;
   }
   float c[2][NT][4] = {};
-#pragma unroll 2
+#pragma unroll(NT <= 2 ? 4 : 2)
   for (int k0 = warp * 32; k0 < p.K; k0 += 256) {
     const int k = k0 + t * 8;
     uint4 xv[4], av[NT];
@@ -171,8 +169,8 @@ __device__ __forceinline__ void shrink_pass(const AdapterArgs& p, const int* ids
 }
 
 // Blocks behind the last row block make the lists of adapters of the product's 256-row tiles.
-template <typename T>
-__global__ void __launch_bounds__(256) adapter_shrink_kernel(const AdapterArgs p) {
+template <typename T, int NT>
+__global__ void __launch_bounds__(256, NT <= 4 ? 2 : 1) adapter_shrink_kernel(const AdapterArgs p) {
   extern __shared__ float red[];
   __shared__ int sid[kTileRows];
   __shared__ int first[8];
@@ -213,10 +211,9 @@ __global__ void __launch_bounds__(256) adapter_shrink_kernel(const AdapterArgs p
   }
   __syncthreads();
   const int per = (p.R + 7) >> 3, tiles = nd * per;
-  for (int t0 = blockIdx.y * kGroup; t0 < tiles; t0 += gridDim.y * kGroup) {
-    const int nt = min(kGroup, tiles - t0), width = nt <= 2 ? 16 : kGroup * 8;
-    if (nt <= 2) shrink_pass<T, 2>(p, sid, t0, nt, red);
-    else shrink_pass<T, kGroup>(p, sid, t0, nt, red);
+  for (int t0 = blockIdx.y * NT; t0 < tiles; t0 += gridDim.y * NT) {
+    const int nt = min(NT, tiles - t0);
+    shrink_pass<T, NT>(p, sid, t0, nt, red);
     __syncthreads();
     // rows x columns of this pass; a row takes the columns of its own adapter
     for (int e = threadIdx.x; e < kShrinkRows * nt * 8; e += 256) {
@@ -224,7 +221,7 @@ __global__ void __launch_bounds__(256) adapter_shrink_kernel(const AdapterArgs p
       if (sid[32 + r] != q / per) continue;
       float s = 0.f;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) s += red[(w * kShrinkRows + r) * width + c];
+      for (int w = 0; w < 8; ++w) s += red[(w * kShrinkRows + r) * (NT * 8) + c];
       const int a = sid[q / per];
       s = j < p.R ? s * (p.scales ? p.scales[a] : 1.f) : 0.f;
       T* t = static_cast<T*>(p.t) + (int64_t)(m0 + r) * 2 * p.Rp + j;
@@ -335,22 +332,29 @@ cudaError_t launch_few(const AdapterArgs& a, cudaStream_t s) {
 
 constexpr int kFewRows = 32;
 
+template <typename T, int NT>
+bool launch_shrink(const AdapterArgs& a, int blocks, int lists, int gy, cudaStream_t s) {
+  constexpr int kBytes = 8 * kShrinkRows * NT * 8 * 4;
+  if (kBytes > 48 * 1024 &&
+      cudaFuncSetAttribute(adapter_shrink_kernel<T, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) != cudaSuccess)
+    return false;
+  adapter_shrink_kernel<T, NT><<<dim3(blocks + lists, gy), 256, kBytes, s>>>(a);
+  return true;
+}
+
 template <typename T>
 cudaError_t launch16(const AdapterArgs& a, int dtype, cudaStream_t s) {
   const int per = (a.R + 7) / 8, most = std::min(a.adapters, std::min(a.M, kShrinkRows)) * per;   // column tiles of a block
-  const int passes = (most + kGroup - 1) / kGroup, blocks = (a.M + kShrinkRows - 1) / kShrinkRows;
+  const int blocks = (a.M + kShrinkRows - 1) / kShrinkRows;
   const bool few = a.M <= kFewRows;
   const int lists = few ? 0 : (a.M + kTileRows - 1) / kTileRows;
-  const int width = most <= 2 ? 16 : kGroup * 8;
-  // a pass each to more blocks while that leaves multiprocessors idle
-  const int gy = std::max(1, std::min(passes, sm_count() * 2 / blocks));
-  const int smem = 8 * kShrinkRows * width * 4;
-  static_assert(8 * kShrinkRows * kGroup * 8 * 4 <= 64 * 1024, "");
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(adapter_shrink_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
-  adapter_shrink_kernel<T><<<dim3(blocks + lists, gy), 256, smem, s>>>(a);
+  // Two tiles to a block while that leaves multiprocessors idle (8 rows with 8 adapters of rank 16: 17 us
+  // with 8 tiles to a block), else one pass over x for all of them, if its registers allow: 4 tiles leave
+  // room for two blocks per multiprocessor (70,144 rows, one adapter of rank 32 in a block: 105 us; 193 us
+  // with 8).
+  if (most <= 2 || (int64_t)blocks * ((most + 1) / 2) <= sm_count()) launch_shrink<T, 2>(a, blocks, lists, (most + 1) / 2, s);
+  else if (a.R <= 32) launch_shrink<T, 4>(a, blocks, lists, 1, s);
+  else if (!launch_shrink<T, 8>(a, blocks, lists, 1, s)) return cudaErrorInvalidValue;
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (!few) return launch_adapter_gemm(a, dtype, s);
