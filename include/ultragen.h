@@ -437,7 +437,9 @@ int ultragen_warm_start(const float* x_lr, const float* noise, float* x_hr, int 
  *   weight, bias  [cols], or [batch, cols] with per_sample, contiguous, of wdtype (dtype or
  *                 F32); each may be NULL
  *   mean, rstd    [batch * rows] F32 outputs, each may be NULL
- * All arithmetic is fp32; y is rounded once.  batch = 0 and rows = 0 do nothing.
+ * All arithmetic is fp32; y is rounded once.  batch = 0 and rows = 0 do nothing.  The calls read
+ * whole 16-byte pieces that hold a row of x or dy, up to 15 bytes before and behind it (which
+ * lie in the same memory page; their values do not matter).
  *   INVALID_ARG: null x / y, a negative size, cols < 1, an unknown type, eps negative or not
  *   finite.  UNSUPPORTED: cols > 16384, batch * rows > 2^31 - 1, batch > 65535 with per_sample.
  *
@@ -476,7 +478,11 @@ int ultragen_layer_norm_backward(const ultragen_norm_t* n, const void* dy, const
  *   scales [adapters] F32 (NULL: 1)
  *   ids [rows] int32: the row's adapter; any value outside [0, adapters) means none.  Rows of
  *                 one adapter need not be neighbours.
- * Sums are fp32; y is rounded once.  rows = 0 does nothing.
+ * Sums are fp32; y is rounded once.  rows = 0 does nothing.  For 16-bit types scales[id] A_id x_m
+ * is held as the sum of two numbers of that type (relative error 2^-16 in bf16, less in fp16, where
+ * it must stay below 65,504).  Infinities and NaN in one adapter reach only its own rows.
+ * Tensor cores serve 16-bit types with k and x_row multiples of 8 and x, w, a on 16 bytes; other
+ * calls take a general kernel, tens of times slower for many rows.
  *   INVALID_ARG: a null pointer, a size < 1 (rows < 0), an unknown type, too little workspace.
  *   UNSUPPORTED: rank > 128, n > 4,194,240.
  */
