@@ -114,17 +114,20 @@ def _norm_sizes(x, weight, bias, plus_one, eps):
         raise ValueError(f"x has shape {tuple(x.shape)}")
     n = NormSizes(batch=B, rows=R, cols=C, dtype=_CODE[x.dtype], wdtype=_CODE[x.dtype],
                   plus_one=1 if plus_one else 0, eps=float(eps), x_row=x3.stride(1), x_batch=x3.stride(0))
-    given = [(t, name) for t, name in ((weight, "weight"), (bias, "bias")) if t is not None]
-    for t, name in given:
-        _tensor(t, name, (x.dtype, torch.float32), device=x.device)
-    if given:
-        t = given[0][0]
-        if t.dim() == 2 and x.dim() != 3:
+    t = bias if weight is None else weight
+    if t is not None:
+        if not isinstance(t, torch.Tensor) or t.dtype not in (x.dtype, torch.float32):
+            raise ValueError("weight and bias must have x's dtype or float32")
+        per_sample = t.dim() == 2
+        if per_sample and x.dim() != 3:
             raise ValueError("a weight per sample needs x [batch, rows, cols]")
-        n.per_sample = 1 if t.dim() == 2 else 0
+        n.per_sample = 1 if per_sample else 0
         n.wdtype = _CODE[t.dtype]
-        for t2, name in given:
-            _contiguous(t2, name, (t.dtype,), (B, C) if n.per_sample else (C,), x.device)
+        shape = (B, C) if per_sample else (C,)
+        if weight is not None:
+            _contiguous(weight, "weight", (t.dtype,), shape, x.device)
+        if bias is not None:
+            _contiguous(bias, "bias", (t.dtype,), shape, x.device)
     return n, x3
 
 

@@ -330,7 +330,9 @@ cudaError_t launch_few(const AdapterArgs& a, cudaStream_t s) {
   return launch_after(adapter_few_kernel<T, NT, RT>, (a.N + 16 * RT - 1) / (16 * RT), 8 * NT * 8 * 16 * RT * 4, a, s);
 }
 
-constexpr int kFewRows = 32;
+// Up to here the rows of x are few enough to pass by every 16 rows of W (2,048 -> 6,144: 33 rows take 27 us,
+// 64 take 33.7; as tensor-core tiles of 256 rows 34 and 33.9).
+constexpr int kFewRows = 64;
 
 template <typename T, int NT>
 bool launch_shrink(const AdapterArgs& a, int blocks, int lists, int gy, cudaStream_t s) {
@@ -358,7 +360,7 @@ cudaError_t launch16(const AdapterArgs& a, int dtype, cudaStream_t s) {
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (!few) return launch_adapter_gemm(a, dtype, s);
-  return a.M <= 8 ? launch_few<T, 1, 1>(a, s) : a.M <= 16 ? launch_few<T, 2, 1>(a, s) : launch_few<T, 4, 1>(a, s);
+  return a.M <= 8 ? launch_few<T, 1, 1>(a, s) : a.M <= 16 ? launch_few<T, 2, 1>(a, s) : a.M <= 32 ? launch_few<T, 4, 1>(a, s) : launch_few<T, 8, 1>(a, s);
 }
 
 int check(const ultragen_adapter_t* c) {

@@ -97,16 +97,17 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
 // The same wait in few instructions, for kernels whose roles together outgrow the instruction cache
 // (every wait's code is fetched along with the code around it): the CTA's abort word in shared memory
 // holds the code of a wait that ran out, which the kernel reports when it ends.  `limit_ns` < 2^31: the
-// 32-bit timer wraps after 4.3 s, and the difference is taken as signed, so that a timer that steps
-// back a little ends no wait.
+// 32-bit timer wraps after 4.3 s, and the difference is taken as signed; a wait also takes 2,048 looks
+// before it runs out.  So a timer that is stepped ends no wait.
 __device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, uint32_t abort_word, int code, uint32_t limit_ns) {
   uint32_t ok;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .u32 t0, t, f;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 t0, t, f, n;\n\t"
       "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %6;\n\t"
       "mov.u32 %0, 1;\n\t"
       "@p bra DONE_%=;\n\t"
-      "mov.u32 t0, %%globaltimer_lo;\n"
+      "mov.u32 t0, %%globaltimer_lo;\n\t"
+      "mov.u32 n, 0;\n"
       "LOOP_%=:\n\t"
       "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %6;\n\t"
       "@p bra DONE_%=;\n\t"
@@ -114,6 +115,8 @@ __device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, u
       "mov.u32 t, %%globaltimer_lo;\n\t"
       "sub.u32 t, t, t0;\n\t"
       "setp.gt.s32 q, t, %5;\n\t"
+      "add.u32 n, n, 1;\n\t"
+      "setp.gt.and.u32 q, n, 2048, q;\n\t"
       "@q st.volatile.shared.u32 [%3], %4;\n\t"
       "setp.ne.or.u32 q, f, 0, q;\n\t"
       "@!q bra LOOP_%=;\n\t"
