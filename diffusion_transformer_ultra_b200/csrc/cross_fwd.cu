@@ -323,12 +323,17 @@ __device__ void softmax_role(const CrossParams& p, float* inv_s, uint32_t tbase,
           if (m == neg_inf() || need) m = mnew;
         }
         const float mu = m == neg_inf() ? 0.f : m;
-        __syncwarp();
-        load_half(tS, s, part_tile, vis.x, vis.y);
-        part = exp_half<T>(s, pa, scale, mu);
-        __syncwarp();
-        load_half(tS + 64, s, part_tile, vis.z, vis.w);
-        part += exp_half<T>(s, pb, scale, mu);
+        part = 0.f;
+#pragma unroll 1                       // (one copy of this code: all roles share the instruction cache)
+        for (int h = 0; h < 2; ++h) {
+          __syncwarp();
+          load_half(tS + 64 * h, s, part_tile, h ? vis.z : vis.x, h ? vis.w : vis.y);
+          part += exp_half<T>(s, pb, scale, mu);
+          if (h == 0) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) pa[c] = pb[c];
+          }
+        }
         if (exact || !__any_sync(0xffffffffu, !(part <= 4096.0f))) break;
         exact = true;
       }
