@@ -86,16 +86,18 @@ struct CfgQ {
   static constexpr int RED_OFF = V_OFF + NV * TILE;            // [2][2][128] floats: halves of a row's sum
   static constexpr int BAR_OFF = RED_OFF + 4 * 128 * 4;
   // full / empty of Q, dO, K (full, scrubbed, empty), V; S ready / read; dP ready; dS ready;
-  // accumulator ready / read; halves exchanged
+  // accumulator ready / read; halves exchanged.  dP and dS of odd and even steps have barriers of their
+  // own: S and dP of step g are issued before dS of step g - 1 is waited for, so that dS of step g may be
+  // there by then, and on one barrier that would be a second phase, behind which the first is not seen.
   static constexpr int B_QF = 0, B_QE = 1, B_OF = 2, B_OE = 3, B_KF = 4, B_KS = B_KF + NK, B_KE = B_KS + NK, B_VF = B_KE + NK,
-                       B_VE = B_VF + NV, B_SF = B_VE + NV, B_SR = B_SF + 1, B_PF = B_SR + 1, B_DS = B_PF + 2, B_AF = B_DS + 1,
+                       B_VE = B_VF + NV, B_SF = B_VE + NV, B_SR = B_SF + 1, B_PF = B_SR + 1, B_DS = B_PF + 2, B_AF = B_DS + 2,
                        B_AE = B_AF + 1, B_XR = B_AE + 1, B_DRAIN = B_XR + 1,
                        NBAR = B_DRAIN + 1;
   static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
   static constexpr int SMEM = MISC_OFF + 16;
   static_assert(SMEM <= 227 * 1024, "shared memory per CTA exceeds 227 KB");
   static __device__ __forceinline__ uint32_t arrivals(int i) {
-    return i == B_SR || i == B_DS || i == B_XR ? 8 : (i == B_AE ? 4 : 1);   // elementwise warps; warps 12-15
+    return i == B_SR || i == B_DS || i == B_DS + 1 || i == B_XR ? 8 : (i == B_AE ? 4 : 1);   // elementwise warps; warps 12-15
   }
 };
 constexpr int kThreadsQ = 512, kRegsLaunchQ = 128, kRegsElemQ = 184, kRegsOtherQ = 72;
@@ -244,7 +246,7 @@ __device__ void dq_mma(const CrossParams& p, uint32_t sbase, uint32_t tbase, con
         if (j == n - 1) mma_commit_elect(bar + 8 * C::B_OE);
       }
       if (pending) {                   // dQ += dS K of step g - 1
-        if (!(ok = wait.warp(C::B_DS, (g - 1) & 1))) break;
+        if (!(ok = wait.warp(C::B_DS + ((g - 1) & 1), ((g - 1) >> 1) & 1))) break;
         if (pfirst && pitem > 0 && !(ok = wait.warp(C::B_AE, (pitem - 1) & 1))) break;
         tc_fence_after();
         mma_accum<T, D>(tAcc, tbase + 128 + 128 * ((g - 1) & 1), sbase + C::K_OFF + pslot * C::TILE, pfirst);
@@ -366,7 +368,7 @@ __device__ void dq_elementwise(const CrossParams& p, float* red, uint32_t tbase,
       tmem_st32(tP + 128 * (g & 1), pk);
       tmem_wait_st();
       tc_fence_before();
-      warp_arrive(bar + 8 * C::B_DS);
+      warp_arrive(bar + 8 * (C::B_DS + (g & 1)));
       ++g;
     }
   }
