@@ -54,7 +54,7 @@ struct NormArgs {
   float* rstd;
   float* part;             // [runs][2][C] sums of the backward pass (null: not wanted)
   int64_t x_row, x_batch, y_row, y_batch, dy_row, dy_batch;
-  int64_t total;           // rows of all samples
+  int64_t total;           // rows of all samples, below 2^31: a row plus a step of the walk fits 32 unsigned bits
   int rows, C;             // rows per sample
   FastDiv div_rows;        // by rows
   int64_t w_batch;         // C with a weight per sample, else 0
@@ -295,12 +295,12 @@ __global__ void __launch_bounds__(NV == 8 ? 544 : 512) norm_fwd_kernel(const Nor
   __shared__ uint32_t abort_word;
   extern __shared__ __align__(16) uint8_t smem[];
   init_bars(bars, &abort_word, 2 * p.at_once * p.slots);
-  const int first = blockIdx.x * p.at_once, r1 = (int)p.total, step = gridDim.x * p.at_once;
+  const uint32_t first = blockIdx.x * p.at_once, r1 = (uint32_t)p.total, step = gridDim.x * p.at_once;
   if (threadIdx.x >= p.at_once * p.warps * 32) {             // producer warp: a lane to a row group
     const int group = threadIdx.x & 31;
     if (group < p.at_once) {
       Ring<T, 1> ring(p, group, bars, smem, &abort_word);
-      for (int row = first + group; row < r1; row += step, ring.next()) {
+      for (uint32_t row = first + group; row < r1; row += step, ring.next()) {
         if (!ring.wait_free()) break;
         const uint32_t s = p.div_rows.div(row), i = row - s * p.rows;
         const T* src[1] = {static_cast<const T*>(p.x) + s * p.x_batch + i * p.x_row};
@@ -314,13 +314,13 @@ __global__ void __launch_bounds__(NV == 8 ? 544 : 512) norm_fwd_kernel(const Nor
   Row<MULTI> me(p, red);
   const Span<CONTIG, NV> at(me.t, p.C);
   Ring<T, 1> ring(p, me.group, bars, smem, &abort_word);
-  const int r0 = first + me.group;
+  const uint32_t r0 = first + me.group;
   float2 w[NV][2], b[NV][2];
   int64_t loaded = -1;                 // whose weight these are
   // Two rows at a time, whose sums share the shuffles and barriers: a row alone is one long chain of
   // them.  (Rows of two samples with a weight each go one by one.)
-  for (int row = r0; row < r1;) {
-    int at_row[2] = {row, row + step};
+  for (uint32_t row = r0; row < r1;) {
+    uint32_t at_row[2] = {row, row + step};
     uint32_t smp[2] = {p.div_rows.div(row), 0};
     bool two = at_row[1] < r1;
     if (two) smp[1] = p.div_rows.div(at_row[1]);
@@ -422,11 +422,11 @@ __global__ void __launch_bounds__(512) norm_wide_kernel(const NormArgs p) {
   extern __shared__ __align__(16) uint8_t smem[];
   init_bars(bars, &abort_word, 2 * p.at_once * p.slots);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int first = blockIdx.x * p.at_once, r1 = (int)p.total, step = gridDim.x * p.at_once;
+  const uint32_t first = blockIdx.x * p.at_once, r1 = (uint32_t)p.total, step = gridDim.x * p.at_once;
   if (warp == p.at_once) {             // producer warp: a lane to a row group
     if (lane < p.at_once) {
       Ring<T, 1> ring(p, lane, bars, smem, &abort_word);
-      for (int row = first + lane; row < r1; row += step, ring.next()) {
+      for (uint32_t row = first + lane; row < r1; row += step, ring.next()) {
         if (!ring.wait_free()) break;
         const uint32_t s = p.div_rows.div(row), i = row - s * p.rows;
         const T* src[1] = {static_cast<const T*>(p.x) + s * p.x_batch + i * p.x_row};
@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(512) norm_wide_kernel(const NormArgs p) {
   Ring<T, 1> ring(p, warp, bars, smem, &abort_word);
   const Span<true, NV> at(lane, p.C);
   const float2 plus = both(p.w ? p.plus : 1.f);
-  for (int row = first + warp; row < r1;) {
+  for (uint32_t row = first + warp; row < r1;) {
     uint32_t smp[2] = {p.div_rows.div(row), 0};
     bool two = row + step < r1;
     if (two) smp[1] = p.div_rows.div(row + step);
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(512) norm_wide_kernel(const NormArgs p) {
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       if (r == 1 && !two) break;
-      const int i = row + r * step - smp[r] * p.rows;
+      const uint32_t i = row + r * step - smp[r] * p.rows;
       if (!ring.wait()) return;
       at.load_row(ring.row(0, static_cast<const T*>(p.x) + smp[r] * p.x_batch + i * p.x_row), v[r]);
 #pragma unroll
@@ -527,13 +527,13 @@ __global__ void __launch_bounds__(NV == 8 ? 544 : 512) norm_bwd_kernel(const Nor
   extern __shared__ __align__(16) uint8_t smem[];
   init_bars(bars, &abort_word, 2 * p.at_once * p.slots);
   const int64_t group = blockIdx.x / p.runs_per_group, run = blockIdx.x - group * p.runs_per_group;
-  const int first = (int)(group * p.group_rows + p.group_rows * run / p.runs_per_group);
-  const int r1 = (int)(group * p.group_rows + p.group_rows * (run + 1) / p.runs_per_group);
+  const uint32_t first = (uint32_t)(group * p.group_rows + p.group_rows * run / p.runs_per_group);
+  const uint32_t r1 = (uint32_t)(group * p.group_rows + p.group_rows * (run + 1) / p.runs_per_group);
   if (threadIdx.x >= p.at_once * p.warps * 32) {             // producer warp: a lane to a row group
     const int g = threadIdx.x & 31;
     if (g < p.at_once) {
       Ring<T, 2> ring(p, g, bars, smem, &abort_word);
-      for (int row = first + g; row < r1; row += p.at_once, ring.next()) {
+      for (uint32_t row = first + g; row < r1; row += p.at_once, ring.next()) {
         if (!ring.wait_free()) break;
         const uint32_t s = p.div_rows.div(row), i = row - s * p.rows;
         const T* src[2] = {static_cast<const T*>(p.x) + s * p.x_batch + i * p.x_row,
@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(NV == 8 ? 544 : 512) norm_bwd_kernel(const Nor
   Row<MULTI> me(p, red);
   const Span<CONTIG, NV> at(me.t, p.C);
   Ring<T, 2> ring(p, me.group, bars, smem, &abort_word);
-  const int r0 = first + me.group;
+  const uint32_t r0 = first + me.group;
   float2 dw[NV][2], db[NV][2], w[NV][2];
 #pragma unroll
   for (int k = 0; k < NV; ++k)
@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(NV == 8 ? 544 : 512) norm_bwd_kernel(const Nor
     mean = __ldg(p.mean + r0);
     rstd = __ldg(p.rstd + r0);
   }
-  for (int row = r0; row < r1; row += p.at_once, ring.next()) {
+  for (uint32_t row = r0; row < r1; row += p.at_once, ring.next()) {
     const uint32_t s = p.div_rows.div(row), i = row - s * p.rows;
     const T* x = ring.row(0, static_cast<const T*>(p.x) + s * p.x_batch + i * p.x_row);
     const T* dy = ring.row(1, static_cast<const T*>(p.dy) + s * p.dy_batch + i * p.dy_row);

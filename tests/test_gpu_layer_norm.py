@@ -293,3 +293,38 @@ def test_gradients_against_differences(ug):
         # mean and rstd come rounded from the forward pass: 4 (C + 4) e relative at most, on top
         extra = 4 * (C + 4) * E * (ref[0].abs() + dy.double().abs().amax()) * d.abs()
         assert abs((got.double() * d).sum() - slope) <= (ref[1] * d.abs()).sum() + extra.sum() + 1e-7 * slope.abs()
+
+
+def test_as_many_rows_as_are_taken(ug):
+    """2^31 - 1 rows of two columns: a row index plus the walk's step passes 2^31.  Sampled rows at the start,
+    in the middle and at the end against the formula; every output is written."""
+    import torch
+    R, C = 2 ** 31 - 1, 2
+    x = torch.empty(R, C, dtype=torch.bfloat16, device="cuda")
+    part = 2 ** 28
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    for i in range(0, R, part):                                # (a fill in parts: the generator's own limits)
+        x[i:i + part].normal_(generator=g)
+    w, b = torch.tensor([1.5, -0.75], device="cuda"), torch.tensor([0.25, -2.0], device="cuda")
+    y = torch.full_like(x, float("nan"))
+    mean, rstd = (torch.full((R,), float("nan"), device="cuda") for _ in range(2))
+    ug.layer_norm(x, y, w, b, eps=1e-3, mean=mean, rstd=rstd)
+    torch.cuda.synchronize()
+    assert ug.operator_status() == 0
+    spots = [slice(i, min(i + 5000, R)) for i in (0, R // 3, 2 ** 30 - 2500, R - 5000)]
+    for s in spots:
+        ry, rm, rr = forward_reference(x[None, s], w, b, 0.0, 1e-3, x.dtype)
+        check("y", y[None, s], ry)
+        check("mean", mean[None, s], rm)
+        check("rstd", rstd[None, s], rr)
+    assert not any(torch.isnan(t[i:i + part]).any() for t in (y, mean, rstd) for i in range(0, R, part))
+    dx, dw = y, torch.full((C,), float("nan"), device="cuda")
+    dx.fill_(float("nan"))
+    ug.layer_norm_backward(x, x, mean, rstd, dx, w, dweight=dw)
+    torch.cuda.synchronize()
+    assert ug.operator_status() == 0 and torch.isfinite(dw).all()
+    for s in spots:
+        check("dx", dx[None, s], backward_reference(x[None, s], x[None, s], mean[None, s], rstd[None, s], w, 0.0, x.dtype,
+                                                    torch.float32, False)[0])
+    assert not any(torch.isnan(dx[i:i + part]).any() for i in range(0, R, part))
