@@ -363,10 +363,14 @@ cudaError_t launch16(const AdapterArgs& a, int dtype, cudaStream_t s) {
   return a.M <= 8 ? launch_few<T, 1, 1>(a, s) : a.M <= 16 ? launch_few<T, 2, 1>(a, s) : a.M <= 32 ? launch_few<T, 4, 1>(a, s) : launch_few<T, 8, 1>(a, s);
 }
 
+constexpr int kMostRows = 0x7fffffff - (kTileRows - 1), kMostColumns = 0x7fffffff - 511;
+
 int check(const ultragen_adapter_t* c) {
   if (!c || c->rows < 0 || c->k < 1 || c->n < 1 || c->rank < 1 || c->adapters < 1) return ULTRAGEN_ERR_INVALID_ARG;
   if (c->dtype != ULTRAGEN_BF16 && c->dtype != ULTRAGEN_F16 && c->dtype != ULTRAGEN_F32) return ULTRAGEN_ERR_INVALID_ARG;
   if (c->rank > 128 || c->n > 65535 * 64) return ULTRAGEN_ERR_UNSUPPORTED;
+  // rows and columns of k are counted in int, up to a tile of rows, or the 8 warps' next pieces of k, behind the last
+  if (c->rows > kMostRows || c->k > kMostColumns) return ULTRAGEN_ERR_UNSUPPORTED;
   return ULTRAGEN_OK;
 }
 

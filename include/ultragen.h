@@ -484,7 +484,7 @@ int ultragen_layer_norm_backward(const ultragen_norm_t* n, const void* dy, const
  * Tensor cores serve 16-bit types with k and x_row multiples of 8 and x, w, a on 16 bytes; other
  * calls take a general kernel, tens of times slower for many rows.
  *   INVALID_ARG: a null pointer, a size < 1 (rows < 0), an unknown type, too little workspace.
- *   UNSUPPORTED: rank > 128, n > 4,194,240.
+ *   UNSUPPORTED: rank > 128, n > 4,194,240, rows > 2^31 - 256, k > 2^31 - 512.
  */
 typedef struct {
   int32_t rows, k, n, rank, adapters, dtype;

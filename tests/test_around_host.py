@@ -82,6 +82,20 @@ def test_adapter_sizes(ffi, mem, bad, status):
     assert L.ultragen_adapter_project(c, a, a, None, a, a, None, a, a, a, 1 << 20, None) == status
 
 
+def test_adapter_sizes_whose_tiles_would_pass_32_bits(ffi, mem):
+    """A tile of rows, or the warps' pieces of k, behind the last one must still have an index."""
+    a, _ = mem
+    L, need = ffi.lib(), ctypes.c_size_t()
+    for most in (dict(rows=2 ** 31 - 256), dict(k=2 ** 31 - 512, x_row=2 ** 31)):
+        c = adapter(ffi, **most)
+        assert L.ultragen_adapter_project_workspace(c, ctypes.byref(need)) == OK and need.value > 0
+        assert L.ultragen_adapter_project(c, a, a, None, a, a, None, a, a, None, 0, None) == INVALID      # (no workspace)
+    for past in (dict(rows=2 ** 31 - 255), dict(rows=2 ** 31 - 1), dict(k=2 ** 31 - 511), dict(k=2 ** 31 - 1)):
+        c = adapter(ffi, **past)
+        assert L.ultragen_adapter_project_workspace(c, ctypes.byref(need)) == UNSUPPORTED
+        assert L.ultragen_adapter_project(c, a, a, None, a, a, None, a, a, a, 1 << 20, None) == UNSUPPORTED
+
+
 def test_adapter_pointers(ffi, mem):
     a, _ = mem
     L, c, need = ffi.lib(), adapter(ffi), ctypes.c_size_t()
