@@ -36,7 +36,6 @@ __device__ int g_error;                // first wait that ran out since the last
 
 constexpr int kThreads = 320;
 constexpr int kWarpProducer = 4, kWarpMma = 5, kWarpExt = 6;
-constexpr uint64_t kDrainNs = 50ull * 1000 * 1000;
 
 template <int BN>
 struct Cfg {
@@ -104,9 +103,7 @@ __device__ void producer_role(const GemmMaps& m, const AdapterArgs& p, uint32_t 
     for (int k = 0; k < nk; ++k, ++st) {
       const uint32_t s = st % C::NS;
       if (!wait(C::B_E + s, ((st / C::NS) & 1) ^ 1)) {
-        // the copies in flight land well within this time; both CTAs stay until then
-        const uint64_t t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < kDrainNs) __nanosleep(1000);
+        settle();                      // both CTAs stay until the copies in flight have landed
         return;
       }
       const uint32_t full = wait.bar + 8 * (C::B_F + s);

@@ -113,7 +113,7 @@ struct Waiter {
 // this CTA exits.
 __device__ __noinline__ inline void settle() {
   const uint64_t t0 = globaltimer_ns();
-  while (globaltimer_ns() - t0 < kDrainNs) __nanosleep(1000);
+  for (uint32_t looks = 0; !wait_over(globaltimer_ns(), t0, kDrainNs, looks); ++looks) __nanosleep(1000);
 }
 
 __device__ __forceinline__ void warp_arrive(uint32_t bar) {

@@ -4,6 +4,8 @@
 
 #include <cstdint>
 
+#include "wait_limit.h"
+
 namespace ug {
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -77,16 +79,16 @@ enum DevErr : int {
 // Bounded wait: sleeps on the barrier phase in slices of 20 us; between slices it checks the
 // CTA abort flag and the wall clock.  Returns false when the CTA is aborting or when
 // `timeout_ns` passed (then it raises the abort flag and records `code` in the global error
-// word).
+// word); see wait_over for the clock.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                           int* err, int code, uint64_t timeout_ns) {
   constexpr uint32_t kSliceNs = 20000;
   if (mbar_try_wait(bar, parity, kSliceNs)) return true;
   const uint64_t t0 = globaltimer_ns();
-  for (;;) {
+  for (uint32_t looks = 1;; ++looks) {
     if (mbar_try_wait(bar, parity, kSliceNs)) return true;
     if (abort_flag && *abort_flag) return false;
-    if (globaltimer_ns() - t0 > timeout_ns) {
+    if (wait_over(globaltimer_ns(), t0, timeout_ns, looks)) {
       if (abort_flag) *abort_flag = 1;
       atomicExch(err, code);
       return false;
@@ -97,8 +99,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
 // The same wait in few instructions, for kernels whose roles together outgrow the instruction cache
 // (every wait's code is fetched along with the code around it): the CTA's abort word in shared memory
 // holds the code of a wait that ran out, which the kernel reports when it ends.  `limit_ns` < 2^31: the
-// 32-bit timer wraps after 4.3 s, and the difference is taken as signed; a wait also takes 2,048 looks
-// before it runs out.  So a timer that is stepped ends no wait.
+// 32-bit timer wraps after 4.3 s; as in wait_over the difference is signed and the looks are counted.
 __device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, uint32_t abort_word, int code, uint32_t limit_ns) {
   uint32_t ok;
   asm volatile(
