@@ -160,6 +160,7 @@ __device__ __forceinline__ void init_bars(uint64_t* bars, uint32_t* abort, int n
   fence_mbar_init();
   __syncthreads();
 }
+// At the end of a warp's work, whichever its role: the producer may be done long before a row's wait runs out.
 __device__ __forceinline__ void report(const uint32_t* abort) {
   const int code = *reinterpret_cast<const volatile int*>(abort);
   if (code == 0) return;
@@ -409,6 +410,7 @@ __global__ void __launch_bounds__(NV == 8 ? 544 : 512) norm_fwd_kernel(const Nor
     }
     row += two ? 2 * step : step;
   }
+  report(&abort_word);
 }
 
 // The forward pass of rows of more than 512 contiguous 16-bit elements, up to 2,048: a warp to a row, so
@@ -451,7 +453,10 @@ __global__ void __launch_bounds__(512) norm_wide_kernel(const NormArgs p) {
     for (int r = 0; r < 2; ++r) {
       if (r == 1 && !two) break;
       const uint32_t i = row + r * step - smp[r] * p.rows;
-      if (!ring.wait()) return;
+      if (!ring.wait()) {
+        report(&abort_word);
+        return;
+      }
       at.load_row(ring.row(0, static_cast<const T*>(p.x) + smp[r] * p.x_batch + i * p.x_row), v[r]);
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
@@ -516,6 +521,7 @@ __global__ void __launch_bounds__(512) norm_wide_kernel(const NormArgs p) {
     }
     row += two ? 2 * step : step;
   }
+  report(&abort_word);
 }
 
 // The same walk; the columns' sums of dy xh and dy stay in registers.
@@ -616,6 +622,7 @@ __global__ void __launch_bounds__(NV == 8 ? 544 : 512) norm_bwd_kernel(const Nor
       at.store(dx, k, out);
     }
   }
+  report(&abort_word);
   if (!p.part) return;
   // the row groups hold sums of the same columns: side by side in the slots' memory, then added in order
   float* out = p.part + (int64_t)blockIdx.x * 2 * p.C;
