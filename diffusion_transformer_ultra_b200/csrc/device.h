@@ -2,8 +2,33 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <mutex>
 
 namespace ug {
+
+// What a kernel needs once on each device before its first launch there (a static of the code that
+// launches it): `set` runs until it succeeds, and no two threads run it at once.
+class OncePerDevice {
+  static constexpr int kMost = 64;
+  std::mutex mu_;
+  bool done_[kMost] = {};
+
+ public:
+  template <typename F>
+  cudaError_t operator()(F set) {
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMost) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mu_);
+    if (done_[dev]) return cudaSuccess;
+    e = set();
+    done_[dev] = e == cudaSuccess;
+    return e;
+  }
+};
 
 // The current device, or ULTRAGEN_ERR_NO_DEVICE when it is not an sm_100 one.
 int current_device(int* dev);

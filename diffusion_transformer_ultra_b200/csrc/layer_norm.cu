@@ -703,12 +703,13 @@ int runs_of(int64_t group_rows, int64_t groups, int sms) {
   return (int)std::max<int64_t>(1, std::min(std::max<int64_t>(1, sms / groups), group_rows));
 }
 
-template <typename K>
-cudaError_t launch_one(K kernel, int blocks, int threads, int smem, const NormArgs& a, cudaStream_t st) {
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
+// (The limit is the most that any call takes, set once: one that followed the call's own size could be
+// lowered by another thread's call before this one's launch.)
+template <auto kernel>
+cudaError_t launch_one(int blocks, int threads, int smem, const NormArgs& a, cudaStream_t st) {
+  static OncePerDevice limit;
+  const cudaError_t e = limit([] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem + kSlack); });
+  if (e != cudaSuccess) return e;
   kernel<<<blocks, threads, smem, st>>>(a);
   return cudaGetLastError();
 }
@@ -716,19 +717,19 @@ cudaError_t launch_one(K kernel, int blocks, int threads, int smem, const NormAr
 template <typename T, typename W>
 cudaError_t launch_wide(const NormArgs& a, int blocks, cudaStream_t st) {
   const int threads = 32 * (a.at_once + 1), smem = smem_bytes(a, false);
-  if (a.C <= 1024) return launch_one(norm_wide_kernel<T, W, 8>, blocks, threads, smem, a, st);
-  if (a.C <= 1536) return launch_one(norm_wide_kernel<T, W, 12>, blocks, threads, smem, a, st);
-  return launch_one(norm_wide_kernel<T, W, 16>, blocks, threads, smem, a, st);
+  if (a.C <= 1024) return launch_one<norm_wide_kernel<T, W, 8>>(blocks, threads, smem, a, st);
+  if (a.C <= 1536) return launch_one<norm_wide_kernel<T, W, 12>>(blocks, threads, smem, a, st);
+  return launch_one<norm_wide_kernel<T, W, 16>>(blocks, threads, smem, a, st);
 }
 
 template <typename T, typename W, bool CONTIG, int NV>
 cudaError_t launch_nv(bool bwd, const NormArgs& a, int blocks, cudaStream_t st) {
   const int threads = 32 * (a.warps * a.at_once + 1), smem = smem_bytes(a, bwd);
   if (!bwd)
-    return a.warps > 1 ? launch_one(norm_fwd_kernel<T, W, CONTIG, NV, true>, blocks, threads, smem, a, st)
-                       : launch_one(norm_fwd_kernel<T, W, CONTIG, NV, false>, blocks, threads, smem, a, st);
-  return a.warps > 1 ? launch_one(norm_bwd_kernel<T, W, CONTIG, NV, true>, blocks, threads, smem, a, st)
-                     : launch_one(norm_bwd_kernel<T, W, CONTIG, NV, false>, blocks, threads, smem, a, st);
+    return a.warps > 1 ? launch_one<norm_fwd_kernel<T, W, CONTIG, NV, true>>(blocks, threads, smem, a, st)
+                       : launch_one<norm_fwd_kernel<T, W, CONTIG, NV, false>>(blocks, threads, smem, a, st);
+  return a.warps > 1 ? launch_one<norm_bwd_kernel<T, W, CONTIG, NV, true>>(blocks, threads, smem, a, st)
+                     : launch_one<norm_bwd_kernel<T, W, CONTIG, NV, false>>(blocks, threads, smem, a, st);
 }
 
 template <typename T, typename W, bool CONTIG>

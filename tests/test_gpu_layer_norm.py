@@ -295,6 +295,39 @@ def test_gradients_against_differences(ug):
         assert abs((got.double() * d).sum() - slope) <= (ref[1] * d.abs()).sum() + extra.sum() + 1e-7 * slope.abs()
 
 
+def test_calls_of_several_threads_that_take_unequal_shared_memory(ug):
+    """The same kernel for many rows and for few, from host threads at once (through the C call, which runs
+    without Python's lock): each launch is accepted."""
+    import ctypes
+    import threading
+    import torch
+    from diffusion_transformer_ultra_b200 import around
+    call = ctypes.CDLL(ug._ffi.LIB_PATH).ultragen_layer_norm
+    call.argtypes = ug.lib().ultragen_layer_norm.argtypes
+    jobs, answers = [], []
+    for R in (2000, 300, 2000, 300):
+        x, _, w, b = make(1, R, 1000, "bf16", "shared")
+        y = torch.empty_like(x)
+        n, _ = around._norm_sizes(x, w, b, False, 1e-6)
+        n.y_row, n.y_batch = y.stride(1), y.stride(0)
+        jobs.append((x, y, w, b, n, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+
+    def work(x, y, w, b, n, stream):
+        torch.cuda.set_device(x.device)
+        args = (ctypes.byref(n), x.data_ptr(), w.data_ptr(), b.data_ptr(), y.data_ptr(), None, None, stream.cuda_stream)
+        answers.append({call(*args) for _ in range(20000)})
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert answers == [{0}] * len(jobs)
+    for x, y, w, b, *_ in jobs:
+        check("y", y, forward_reference(x, w, b, 0.0, 1e-6, x.dtype)[0])
+
+
 def test_as_many_rows_as_are_taken(ug):
     """2^31 - 1 rows of two columns: a row index plus the walk's step passes 2^31.  Sampled rows at the start,
     in the middle and at the end against the formula; every output is written."""
