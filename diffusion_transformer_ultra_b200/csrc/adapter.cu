@@ -335,13 +335,17 @@ cudaError_t launch_few(const AdapterArgs& a, cudaStream_t s) {
 constexpr int kFewRows = 64;
 
 template <typename T, int NT>
-bool launch_shrink(const AdapterArgs& a, int blocks, int lists, int gy, cudaStream_t s) {
+cudaError_t launch_shrink(const AdapterArgs& a, int blocks, int lists, int gy, cudaStream_t s) {
   constexpr int kBytes = 8 * kShrinkRows * NT * 8 * 4;
-  if (kBytes > 48 * 1024 &&
-      cudaFuncSetAttribute(adapter_shrink_kernel<T, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) != cudaSuccess)
-    return false;
+  if (kBytes > 48 * 1024) {
+    static OncePerDevice limit;
+    const cudaError_t e = limit([] {
+      return cudaFuncSetAttribute(adapter_shrink_kernel<T, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+    });
+    if (e != cudaSuccess) return e;
+  }
   adapter_shrink_kernel<T, NT><<<dim3(blocks + lists, gy), 256, kBytes, s>>>(a);
-  return true;
+  return cudaGetLastError();
 }
 
 template <typename T>
@@ -354,10 +358,8 @@ cudaError_t launch16(const AdapterArgs& a, int dtype, cudaStream_t s) {
   // with 8 tiles to a block), else one pass over x for all of them, if its registers allow: 4 tiles leave
   // room for two blocks per multiprocessor (70,144 rows, one adapter of rank 32 in a block: 105 us; 193 us
   // with 8).
-  if (most <= 2 || (int64_t)blocks * ((most + 1) / 2) <= sm_count()) launch_shrink<T, 2>(a, blocks, lists, (most + 1) / 2, s);
-  else if (a.R <= 32) launch_shrink<T, 4>(a, blocks, lists, 1, s);
-  else if (!launch_shrink<T, 8>(a, blocks, lists, 1, s)) return cudaErrorInvalidValue;
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = most <= 2 || (int64_t)blocks * ((most + 1) / 2) <= sm_count() ? launch_shrink<T, 2>(a, blocks, lists, (most + 1) / 2, s)
+                        : a.R <= 32 ? launch_shrink<T, 4>(a, blocks, lists, 1, s) : launch_shrink<T, 8>(a, blocks, lists, 1, s);
   if (e != cudaSuccess) return e;
   if (!few) return launch_adapter_gemm(a, dtype, s);
   return a.M <= 8 ? launch_few<T, 1, 1>(a, s) : a.M <= 16 ? launch_few<T, 2, 1>(a, s) : a.M <= 32 ? launch_few<T, 4, 1>(a, s) : launch_few<T, 8, 1>(a, s);
