@@ -1,9 +1,9 @@
 """Operators around the joint attention: layer norm, the projection with low-rank adapters, and
 cross attention to an encoder's states.  Argument marshalling only, as in ``_ffi``: every step
 runs in the library's kernels, on the tensors' device and on ``stream`` (default: the current
-stream of that device).  Outputs are tensors of the caller; scratch memory comes from PyTorch's
-allocator on that stream, so calls on different streams, and graphs captured from them, never
-share it.
+stream of that device).  Outputs are tensors of the caller, which overlap no other operand except
+where a call says that they may be one; scratch memory comes from PyTorch's allocator on that
+stream, so calls on different streams, and graphs captured from them, never share it.
 """
 from __future__ import annotations
 
@@ -273,7 +273,7 @@ def cross_attention(q, k, v, o, kv_lens=None, key_mask=None, scale=None, lse=Non
     k, v [batch, ns, kv_heads, D] (bf16 or fp16, D 64 or 128, heads a multiple of kv_heads; any
     strides that are multiples of 16 bytes).  kv_lens [batch] int32 leaves keys [0, kv_lens[b])
     visible, key_mask [batch, ns] (bool) those that are true; hidden keys and values may hold
-    anything.  A query without a visible key gets zeros.  scale defaults to D^-1/2; lse
+    anything.  A query without a visible key gets zeros.  o may be q.  scale defaults to D^-1/2; lse
     [batch, heads, nq] fp32 receives the log-sum-exp the backward pass needs."""
     c = _cross_sizes(q, k, v, kv_lens, key_mask, scale)
     _tensor(o, "o", (q.dtype,), q.shape, q.device)

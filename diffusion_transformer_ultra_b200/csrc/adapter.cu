@@ -418,6 +418,7 @@ int ultragen_adapter_project(const ultragen_adapter_t* c, const void* x, const v
   if (!x || !w || !a || !b || !ids || !y || !workspace || !aligned(workspace) ||
       workspace_bytes < t_bytes(c) + list_bytes(c))
     return ULTRAGEN_ERR_INVALID_ARG;
+  if (begins_at(y, {x, w, bias, a, b, scales, ids, workspace})) return ULTRAGEN_ERR_INVALID_ARG;   // (x is read for every column tile of y)
   int dev;
   if ((st = current_device(&dev)) != ULTRAGEN_OK) return st;
   AdapterArgs p = {};

@@ -267,6 +267,9 @@ int ultragen_cross_attention(const ultragen_cross_t* c, const void* q, const voi
   if (!q || !o || (c->ns > 0 && (!k || !v)) || (key_mask && !c->masked)) return ULTRAGEN_ERR_INVALID_ARG;
   if (!aligned(q, c->stride[0]) || !aligned(o, c->stride[3])) return ULTRAGEN_ERR_INVALID_ARG;
   if (c->ns > 0 && (!aligned(k, c->stride[1]) || !aligned(v, c->stride[2]))) return ULTRAGEN_ERR_INVALID_ARG;
+  // o may be q: an item reads its query tiles whole before it writes their rows
+  if (begins_at(o, {k, v, lse, workspace}) || (o == q && !std::equal(c->stride[0], c->stride[0] + 3, c->stride[3])))
+    return ULTRAGEN_ERR_INVALID_ARG;
   if (c->ns == 0) key_mask = nullptr;
   CrossParams p = {};
   const Layout l = forward_layout(c, p);
@@ -328,6 +331,10 @@ int ultragen_cross_attention_backward(const ultragen_cross_t* c, const void* d_o
   if (c->ns > 0 && (!aligned(k, sd[1]) || !aligned(v, sd[2]) || !aligned(dk, sd[6]) || !aligned(dv, sd[7])))
     return ULTRAGEN_ERR_INVALID_ARG;
   if (key_mask && !c->masked) return ULTRAGEN_ERR_INVALID_ARG;
+  // dq is written before the pass that makes dk and dv reads q, k, v and do; those are read for every key tile
+  if (begins_at(dq, {q, k, v, d_o, dk, dv, lse, workspace}) || begins_at(dk, {q, d_o, dv, workspace}) ||
+      begins_at(dv, {q, d_o, workspace}))
+    return ULTRAGEN_ERR_INVALID_ARG;
   if (c->ns == 0) key_mask = nullptr;
   CrossParams p = {};
   const Layout l = backward_layout(c, p);

@@ -4,9 +4,18 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <initializer_list>
 #include <mutex>
 
 namespace ug {
+
+// Whether an output begins where one of the other operands does (null: not there).  Overlap that begins
+// elsewhere is the caller's to avoid: strided tensors may lie between one another's rows.
+inline bool begins_at(const void* out, std::initializer_list<const void*> others) {
+  for (const void* p : others)
+    if (out && out == p) return true;
+  return false;
+}
 
 // What a kernel needs once on each device before its first launch there (a static of the code that
 // launches it): `set` runs until it succeeds, and no two threads run it at once.

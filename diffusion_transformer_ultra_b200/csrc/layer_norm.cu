@@ -771,6 +771,12 @@ int check(const ultragen_norm_t* n) {
   return ULTRAGEN_OK;
 }
 
+// Whether a tensor with strides (row, batch) at `p` is all of another at `q`: the same elements at the same
+// places, so that an output may replace it, or has no element in common with its first.
+bool same_or_apart(const ultragen_norm_t* n, const void* p, int64_t row, int64_t batch, const void* q, int64_t qrow, int64_t qbatch) {
+  return p != q || ((n->rows == 1 || row == qrow) && (n->batch == 1 || batch == qbatch));
+}
+
 // Whether an operand's rows start on `bytes`.
 bool starts_on(const void* p, int64_t row, int64_t batch, int bytes, int dtype) {
   const int e = elem_size(dtype);
@@ -827,6 +833,9 @@ int ultragen_layer_norm(const ultragen_norm_t* n, const void* x, const void* wei
   if (st != ULTRAGEN_OK) return st;
   if (n->batch == 0 || n->rows == 0) return ULTRAGEN_OK;
   if (!x || !y) return ULTRAGEN_ERR_INVALID_ARG;
+  if (!same_or_apart(n, y, n->y_row, n->y_batch, x, n->x_row, n->x_batch) || begins_at(y, {weight, bias, mean, rstd}) ||
+      begins_at(mean, {rstd}))
+    return ULTRAGEN_ERR_INVALID_ARG;
   int dev;
   if ((st = current_device(&dev)) != ULTRAGEN_OK) return st;
   NormArgs a = args_of(n);
@@ -879,6 +888,10 @@ int ultragen_layer_norm_backward(const ultragen_norm_t* n, const void* dy, const
     return ULTRAGEN_OK;
   }
   if (!dy || !x || !mean || !rstd || !dx) return ULTRAGEN_ERR_INVALID_ARG;
+  if (!same_or_apart(n, dx, n->y_row, n->y_batch, x, n->x_row, n->x_batch) ||
+      !same_or_apart(n, dx, n->y_row, n->y_batch, dy, n->dy_row, n->dy_batch) ||
+      begins_at(dx, {weight, mean, rstd, dweight, dbias}) || begins_at(dweight, {dbias}))
+    return ULTRAGEN_ERR_INVALID_ARG;
   if ((st = current_device(&dev)) != ULTRAGEN_OK) return st;
   const bool contig = contiguous_pieces(n, x, dy, dx, weight, nullptr);
   const Spread sp = spread(n->cols);

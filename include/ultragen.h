@@ -422,7 +422,9 @@ int ultragen_warm_start(const float* x_lr, const float* noise, float* x_hr, int 
  * carry a low-rank adapter for the LR tokens ([UG-note] 关键设计 3) inside an MMDiT block; the
  * calls below are what stands directly in front of it and beside it.  They take strided
  * tensors: every stride is in elements, the last dimension is contiguous, and no operand may
- * overlap itself.  They hold no state between calls: a call that needs scratch memory takes a
+ * overlap itself.  No output may overlap another operand, except where a call says that it may be
+ * one (then at the same address with the same strides); one that begins where an operand does that
+ * it may not be is INVALID_ARG.  They hold no state between calls: a call that needs scratch memory takes a
  * workspace (16-byte aligned device memory of at least the bytes its _workspace function
  * returns for the same sizes on the same device), which it may overwrite and which must not be
  * shared by calls that overlap on the GPU.  Sizes of zero are allowed where noted.
@@ -507,7 +509,7 @@ int ultragen_adapter_project(const ultragen_adapter_t* c, const void* x, const v
  *                 to [0, ns]); key_mask [batch, ns] bytes or NULL: nonzero = visible.  What
  *                 hidden keys and values hold does not matter (NaN included).
  *   lse           [batch, heads, nq] F32 or NULL: log(sum_j exp(scale q_i . k_j)), natural
- *   A query without a visible key gets o = 0 and lse = -inf.
+ *   A query without a visible key gets o = 0 and lse = -inf.  o may be q.
  * ultragen_cross_attention_backward -- the gradients of a loss with d_o = dLoss/do; o and lse as
  *   the forward pass wrote them.  Hidden keys and values get zeros; a query without a visible
  *   key gets dq = 0.  dk and dv of a shared head are summed over its query heads.  Results do

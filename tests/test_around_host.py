@@ -5,6 +5,8 @@ import math
 
 import pytest
 
+from conftest import has_gpu
+
 OK, INVALID, UNSUPPORTED = 0, 1, 2
 
 
@@ -153,6 +155,73 @@ def test_cross_pointers_and_strides(ffi, mem):
             assert L.ultragen_cross_attention(c, a, a, a, None, None, a, None, a, 1 << 20, None) == INVALID
         assert L.ultragen_cross_attention_backward(c, a, a, a, a, a, a, None, None, a, a, a, a, 1 << 20, None) == INVALID
     assert L.ultragen_cross_attention(cross(ffi, batch=0), *[None] * 8, 0, None) == OK
+
+
+def test_an_output_that_is_an_operand(ffi):
+    """Outputs that begin where an operand does that the call still reads are refused; the pairs that the
+    header allows get past the checks (to the device, of which there need be none)."""
+    L, need = ffi.lib(), ctypes.c_size_t()
+    buf = ctypes.create_string_buffer(1 << 16)
+    base = ctypes.addressof(buf) + (-ctypes.addressof(buf)) % 16
+    names = iter(range(64))
+
+    def place():
+        return base + 16 * next(names)
+    x, y, w, b, mean, rstd, dy, dw, db = (place() for _ in range(9))
+    n = norm(ffi)
+    fwd = dict(x=x, w=w, b=b, y=y, mean=mean, rstd=rstd)
+
+    def forward(n=n, **kw):
+        q = dict(fwd, **kw)
+        return L.ultragen_layer_norm(n, *(q[k] for k in ("x", "w", "b", "y", "mean", "rstd")), None)
+    for other in ("w", "b", "mean", "rstd"):
+        assert forward(y=fwd[other]) == INVALID
+    assert forward(mean=rstd) == INVALID
+    assert forward(norm(ffi, y_row=65), y=x) == INVALID and forward(norm(ffi, y_batch=256), y=x) == INVALID
+    bwd = dict(dy=dy, x=x, w=w, mean=mean, rstd=rstd, dx=y, dw=None, db=None)
+
+    def backward(n=n, ws=None, **kw):
+        q = dict(bwd, **kw)
+        return L.ultragen_layer_norm_backward(n, *(q[k] for k in ("dy", "x", "w", "mean", "rstd", "dx", "dw", "db")), 1, ws,
+                                              1 << 20 if ws else 0, None)
+    for other in ("w", "mean", "rstd"):
+        assert backward(dx=bwd[other]) == INVALID
+    assert backward(norm(ffi, y_row=65), dx=x) == INVALID and backward(norm(ffi, dy_row=65), dx=dy) == INVALID
+    assert backward(ws=base, dw=dw, db=dw) == INVALID and backward(ws=base, dx=dw, dw=dw, db=db) == INVALID
+    c = adapter(ffi)
+    assert L.ultragen_adapter_project_workspace(c, ctypes.byref(need)) == OK
+    order = ("x", "w", "bias", "a", "b", "scales", "ids")
+    ops = {k: place() for k in order}
+    ws = place()
+    for other in order:
+        assert L.ultragen_adapter_project(c, *(ops[k] for k in order), ops[other], ws, need.value, None) == INVALID
+    q, k, v, o, do, dq, dk, dv, lse = (place() for _ in range(9))
+    c = cross(ffi, nq=7, kv_heads=4, batch=200)                # (enough items: no workspace forward)
+    assert L.ultragen_cross_attention_workspace(c, 0, ctypes.byref(need)) == OK and need.value == 0
+
+    def attend(c=c, out=o):
+        return L.ultragen_cross_attention(c, q, k, v, None, None, out, lse, None, 0, None)
+    assert attend(out=k) == INVALID and attend(out=v) == INVALID and attend(out=lse) == INVALID
+    other = cross(ffi, nq=7, kv_heads=4, batch=200)
+    other.stride[3][1] = 512
+    assert attend(other, out=q) == INVALID
+    assert L.ultragen_cross_attention_workspace(c, 1, ctypes.byref(need)) == OK
+    back = dict(do=do, q=q, k=k, v=v, o=o, lse=lse, dq=dq, dk=dk, dv=dv)
+
+    def grad(**kw):
+        p = dict(back, **kw)
+        return L.ultragen_cross_attention_backward(c, p["do"], p["q"], p["k"], p["v"], p["o"], p["lse"], None, None, p["dq"], p["dk"],
+                                                   p["dv"], ws, need.value, None)
+    for other in ("q", "k", "v", "do", "dk", "dv", "lse"):
+        assert grad(dq=back[other]) == INVALID
+    for out in ("dk", "dv"):
+        for other in ("q", "do"):
+            assert grad(**{out: back[other]}) == INVALID
+    assert grad(dk=dv) == INVALID
+    if not has_gpu():                                          # (host addresses: nothing may be launched)
+        NO_DEVICE = 7
+        assert forward() == forward(y=x) == backward() == backward(dx=x) == backward(dx=dy) == NO_DEVICE
+        assert attend() == attend(out=q) == grad() == NO_DEVICE
 
 
 def test_binding_refuses_host_tensors():

@@ -255,6 +255,17 @@ def test_without_lse_and_on_a_side_stream(ug):
     assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("shape", [(4, 3000, 300, 24, 24, 64), (2, 300, 700, 4, 2, 128), (1, 500, 300, 5, 1, 128), (2, 1, 2000, 8, 2, 128)])
+def test_output_in_place_of_the_queries(ug, shape):
+    """o may be q: one and two query tiles to an item, split keys, heads that share keys."""
+    import torch
+    q, k, v, _ = inputs(*shape, torch.bfloat16)
+    want = torch.empty_like(q)
+    ug.cross_attention(q, k, v, want)
+    ug.cross_attention(q, k, v, q)
+    assert torch.equal(q, want)
+
+
 def test_empty_sequences(ug):
     import torch
     q, k, v, do = inputs(2, 5, 0, 4, 2, 64, torch.bfloat16)
