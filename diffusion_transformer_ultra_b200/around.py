@@ -93,9 +93,10 @@ def _stream(device):
 
 def operator_status(stream=None) -> int:
     """Waits for `stream` (default: the current one), then returns and clears the device-side
-    status of this module's operators on the current device (0: no kernel's wait ran out)."""
+    status of this module's operators on the stream's device (0: no kernel's wait ran out)."""
     s = torch.cuda.current_stream() if stream is None else stream
-    return lib().ultragen_operator_status(s.cuda_stream)
+    with torch.cuda.device(s.device):
+        return lib().ultragen_operator_status(s.cuda_stream)
 
 
 # ------------------------------------------------------------------------------- layer norm

@@ -239,3 +239,41 @@ def test_binding_refuses_host_tensors():
         ug.cross_attention(q, q, q, q)
     with pytest.raises(ValueError, match="CUDA"):
         ug.cross_attention_backward(q, q, q, q, q, q, q, q, q)
+
+
+@pytest.fixture()
+def devices(monkeypatch):
+    """Two devices without a GPU: the current one is a list's only entry, streams know theirs."""
+    import contextlib
+    import torch
+    current = [torch.device("cuda", 0)]
+
+    @contextlib.contextmanager
+    def device(d):
+        before, current[0] = current[0], torch.device(d)
+        yield
+        current[0] = before
+
+    class Stream:
+        def __init__(self, index):
+            self.device, self.cuda_stream = torch.device("cuda", index), 100 + index
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0].index)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: Stream((current[0] if d is None else torch.device(d)).index))
+    return current, Stream
+
+
+def test_status_is_asked_of_the_streams_device(ffi, devices, monkeypatch):
+    import diffusion_transformer_ultra_b200 as ug
+    from diffusion_transformer_ultra_b200 import around
+    current, stream = devices
+    asked = []
+
+    class Library:
+        @staticmethod
+        def ultragen_operator_status(s):
+            asked.append((current[0].index, s))
+            return 0
+    monkeypatch.setattr(around, "lib", lambda: Library)
+    assert ug.operator_status() == ug.operator_status(stream(1)) == ug.operator_status(stream(0)) == 0
+    assert asked == [(0, 100), (1, 101), (0, 100)] and current[0].index == 0
