@@ -343,10 +343,13 @@ class ProjectedLayer:
         """x [batch, N_raster, channels] bf16, o [batch, N_raster, heads, head_dim]; w, a, b (and bias)
         are triples for Q, K and V as adapter_project takes them; ids [batch * N_raster]; weight and
         shift are the norm's weight and bias."""
-        layer_norm(x, self.norm, weight, shift, eps=eps, plus_one=plus_one, stream=stream)
-        for i, out in enumerate((self.q, self.k, self.v)):
-            self.project(w[i], out, a[i], b[i], ids, scales, None if bias is None else bias[i], stream)
-        return self.layer(self.q, self.k, self.v, o, stream)
+        if not isinstance(o, torch.Tensor) or o.device != self.norm.device:
+            raise ValueError(f"o must be on {self.norm.device}")
+        with _on(self.norm.device, stream):     # `Layer` runs on the current device
+            layer_norm(x, self.norm, weight, shift, eps=eps, plus_one=plus_one, stream=stream)
+            for i, out in enumerate((self.q, self.k, self.v)):
+                self.project(w[i], out, a[i], b[i], ids, scales, None if bias is None else bias[i], stream)
+            return self.layer(self.q, self.k, self.v, o, stream)
 
     def cross(self, o, w, a, b, ids, k, v, scales=None, bias=None, kv_lens=None, key_mask=None, lse=None,
               stream=None):

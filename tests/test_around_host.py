@@ -277,3 +277,30 @@ def test_status_is_asked_of_the_streams_device(ffi, devices, monkeypatch):
     monkeypatch.setattr(around, "lib", lambda: Library)
     assert ug.operator_status() == ug.operator_status(stream(1)) == ug.operator_status(stream(0)) == 0
     assert asked == [(0, 100), (1, 101), (0, 100)] and current[0].index == 0
+
+
+def test_a_projected_layer_runs_on_its_own_device(devices, monkeypatch):
+    """Every step, the joint attention's too, with the buffers' device current; an output elsewhere is refused."""
+    import types
+    import torch
+    from diffusion_transformer_ultra_b200 import around
+    current, _ = devices
+    ran = []
+    one, zero = torch.device("cuda", 1), torch.device("cuda", 0)
+
+    class Fake(torch.Tensor):
+        device = one
+    pl = object.__new__(around.ProjectedLayer)
+    pl.norm = types.SimpleNamespace(device=one, view=lambda *s: None)
+    pl.shape = (1, 2, 3, 4)
+    pl.q = pl.k = pl.v = pl.xq = types.SimpleNamespace(view=lambda *s: None)
+    pl.layer = lambda q, k, v, o, stream: ran.append(("layer", current[0])) or o
+    monkeypatch.setattr(around, "layer_norm", lambda *a, **k: ran.append(("norm", current[0])))
+    monkeypatch.setattr(around, "adapter_project", lambda *a, **k: ran.append(("project", current[0])))
+    o = torch.zeros(1).as_subclass(Fake)
+    three = [None] * 3
+    assert pl(None, o, three, three, three, None) is o
+    assert ran == [("norm", one)] + [("project", one)] * 3 + [("layer", one)] and current[0] == zero
+    with pytest.raises(ValueError, match="cuda:1"):
+        pl(None, torch.zeros(1), three, three, three, None)
+    assert len(ran) == 5
