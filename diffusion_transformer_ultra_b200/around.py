@@ -3,7 +3,8 @@ cross attention to an encoder's states.  Argument marshalling only, as in ``_ffi
 runs in the library's kernels, on the tensors' device and on ``stream`` (default: the current
 stream of that device).  Outputs are tensors of the caller, which overlap no other operand except
 where a call says that they may be one; scratch memory comes from PyTorch's allocator on that
-stream, so calls on different streams, and graphs captured from them, never share it.
+stream, so calls of these functions on different streams, and graphs captured from them, never
+share it.  (A `ProjectedLayer` keeps buffers of its own: see there.)
 """
 from __future__ import annotations
 
@@ -320,8 +321,11 @@ def cross_attention_backward(do, q, k, v, o, lse, dq, dk, dv, kv_lens=None, key_
 class ProjectedLayer:
     """One attention layer from hidden states: layer norm (modulated per sample), the Q, K and V
     projections with each token's adapter beside them, the joint attention of `Layer`, and, where
-    states are given, cross attention of the normed tokens' queries to an encoder's states.  The
-    buffers stay resident between calls; every step runs on `stream`."""
+    states are given, cross attention of the normed tokens' queries to an encoder's states.  Every
+    step runs on `stream`.  The buffers between the steps belong to the instance and stay resident, as
+    `Layer`'s and its plan's do, so calls of one instance, and replays of graphs captured from it, must
+    follow one another: on one stream, or with an event between streams.  cross() reads what the last
+    call normed, so it runs behind that call.  Layers that run at once need an instance and a plan each."""
 
     def __init__(self, plan, batch: int, channels: int, device="cuda"):
         i = plan.info

@@ -124,3 +124,37 @@ def test_refusals(ug):
         with pytest.raises((ValueError, ug.UltragenError)):
             call()
             raise AssertionError(f"case {n} was taken")
+
+
+def test_two_instances_at_once_and_one_behind_an_event(ug):
+    """Instances with a plan each overlap on two streams; one instance moves to another stream behind an event."""
+    import torch
+    sets = []
+    for i in range(2):
+        wl, plan, s = make(ug)
+        if i:
+            s["x"] = s["x"].flip(0).contiguous()
+        pl = ug.ProjectedLayer(plan, wl.batch, s["x"].shape[-1])
+        want = [torch.empty(pl.shape, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        run(ug, pl, s, *want)
+        sets.append((pl, s, want, torch.cuda.Stream(), [[torch.zeros_like(w) for w in want] for _ in range(10)]))
+    torch.cuda.synchronize()
+    assert not torch.equal(sets[0][2][0], sets[1][2][0])
+    for k in range(10):
+        for pl, s, _, st, outs in sets:
+            run(ug, pl, s, *outs[k], stream=st)
+    torch.cuda.synchronize()
+    for _, _, want, _, outs in sets:
+        assert all(torch.equal(a, b) for out in outs for a, b in zip(want, out))
+    (pl, s, want, first, outs), second = sets[0], sets[1][3]
+    last = torch.cuda.Event()
+    for k, st in enumerate((first, second) * 5):
+        for o in outs[k]:
+            o.zero_()
+        st.wait_stream(torch.cuda.current_stream())
+        if k:
+            st.wait_event(last)
+        run(ug, pl, s, *outs[k], stream=st)
+        last.record(st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for out in outs for a, b in zip(want, out))
