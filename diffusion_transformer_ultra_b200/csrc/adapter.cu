@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(256, NT <= 4 ? 2 : 1) adapter_shrink_kernel(co
       T* t = static_cast<T*>(p.t) + (int64_t)(m0 + r) * 2 * p.Rp + j;
       const T hi = from_f32<T>(s);
       t[0] = hi;
-      t[p.Rp] = from_f32<T>(fabsf(to_f32(hi)) < INFINITY ? s - to_f32(hi) : 0.f);
+      t[p.Rp] = from_f32<T>(fabsf(to_f32(hi)) < INFINITY ? (s - to_f32(hi)) * kLowScale<T> : 0.f);
       if (per * 8 < p.Rp && q % per == per - 1) {            // the columns up to Rp
         t[8] = from_f32<T>(0.f);
         t[p.Rp + 8] = from_f32<T>(0.f);
@@ -299,10 +299,10 @@ __global__ void __launch_bounds__(256) adapter_few_kernel(const AdapterArgs p) {
           load_f32<T, 8>(tt + r, hi);
           load_f32<T, 8>(tt + p.Rp + r, lo);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) s += (hi[q] + lo[q]) * bv[q];
+          for (int q = 0; q < 8; ++q) s += (hi[q] + lo[q] * (1.0f / kLowScale<T>)) * bv[q];
         }
       } else {
-        for (int r = 0; r < p.R; ++r) s += (to_f32(tt[r]) + to_f32(tt[p.Rp + r])) * to_f32(b[r]);
+        for (int r = 0; r < p.R; ++r) s += (to_f32(tt[r]) + to_f32(tt[p.Rp + r]) * (1.0f / kLowScale<T>)) * to_f32(b[r]);
       }
     }
     if (p.bias) s += to_f32(static_cast<const T*>(p.bias)[n]);

@@ -5,9 +5,9 @@
 // 128 x BN x 64 products.  (Alone, a CTA would bring 128 + BN rows for them, half as much again,
 // and the loads from L2, not the products, would set the pace.)
 // The adapters are more columns of the same sum, in granules of 16: for each adapter a that rows
-// of the tile use, t_m = s_a A_a x_m (from a kernel before, as the sum of two 16-bit numbers, so
-// that its rounding, 2^-16 at most, does not show in y) in the rows that use it and zero in
-// the others, against B_a; and one granule whose first column is 1 against the bias.
+// of the tile use, t_m = s_a A_a x_m (from a kernel before, as two 16-bit numbers, so that its
+// rounding does not show in y: see kLowScale) in the rows that use it and zero in the others, against
+// B_a (the low parts against B_a / kLowScale); and one granule whose first column is 1 against the bias.
 //
 // Roles per CTA (10 warps): 0-3 epilogue (TMEM -> 16 bits -> shared memory -> rows of y), 4 TMA
 // producer, 5 MMA issuer (first CTA of the pair), 6-9 extension: writes the granules.
@@ -226,6 +226,15 @@ __device__ void extension_role(const AdapterArgs& p, uint8_t* smem, uint32_t sba
 #pragma unroll
               for (int r = 0; r < 8; ++r) bv[r] = 0u;
             }
+            if constexpr (kLowScale<T> != 1.0f)
+              if (sub >= half) {
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                  __half2 h = *reinterpret_cast<__half2*>(&bv[r]);
+                  h = __hmul2(h, __float2half2_rn(1.0f / kLowScale<T>));
+                  bv[r] = *reinterpret_cast<uint32_t*>(&h);
+                }
+              }
           }
         }
         const int c0 = ((2 * k) ^ (i & 7)) * 16, c1 = ((2 * k + 1) ^ (i & 7)) * 16;    // 128-byte swizzle
@@ -259,7 +268,7 @@ __device__ __noinline__ float odd_terms(const T* b, const T* t, int R, int Rp) {
     for (int r = r0; r < min(R, r0 + 16); ++r) {
       const float x = to_f32(b[r]);
       fin = fin && fabsf(x) < INFINITY;
-      s += (to_f32(t[r]) + to_f32(t[Rp + r])) * x;
+      s += (to_f32(t[r]) + to_f32(t[Rp + r]) * (1.0f / kLowScale<T>)) * x;
     }
     if (!fin) v += s;
   }

@@ -481,8 +481,9 @@ int ultragen_layer_norm_backward(const ultragen_norm_t* n, const void* dy, const
  *   ids [rows] int32: the row's adapter; any value outside [0, adapters) means none.  Rows of
  *                 one adapter need not be neighbours.
  * Sums are fp32; y is rounded once.  rows = 0 does nothing.  For 16-bit types scales[id] A_id x_m
- * is held as the sum of two numbers of that type (relative error 2^-16 in bf16, less in fp16, where
- * it must stay below 65,504).  Infinities and NaN in one adapter reach only its own rows.
+ * is held in two numbers of that type.  Called t, it is off by 2^-16 |t| in bf16, and in fp16, where it
+ * must stay below 65,504, by 2^-22 |t| + 2^-36; an fp16 term t b of a sum by min(2^-26 |t|, 2^-12 |t b|)
+ * on top.  Infinities and NaN in one adapter reach only its own rows.
  * Tensor cores serve 16-bit types with k and x_row multiples of 8 and x, w, a on 16 bytes; other
  * calls take a general kernel, tens of times slower for many rows.
  *   INVALID_ARG: a null pointer, a size < 1 (rows < 0), an unknown type, too little workspace.

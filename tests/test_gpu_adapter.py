@@ -222,3 +222,31 @@ def test_rows_past_32_bit_offsets(ug):
     s["x"] = xf
     ug.adapter_project(xf, s["w"], yf, s["a"], s["b"], s["ids"], scales=s["scales"], bias=s["bias"])
     check(yf, *ref)
+
+
+@pytest.mark.parametrize("M", [24, 600])
+@pytest.mark.parametrize("tsize,bsize", [(2.0 ** -18, 1024.0), (2.0 ** -10, 64.0), (2.0 ** 9, 2.0 ** -13), (2.0 ** -4, 1.0)])
+def test_fp16_products_of_unequal_sizes(ug, M, tsize, bsize):
+    """s A x far below B, where a 16-bit low part alone would end at fp16's smallest step, and far above it.
+    The adapter's terms alone (W = 0): each t b is off by what the header states, 2^-22 |t b| + 2^-36 |b| +
+    min(2^-26 |t|, 2^-12 |t b|); the fp32 sums that make t by K 2^-23 of their absolute products, those over
+    the rank by (2 R + K) 2^-23; y is rounded once."""
+    import torch
+    K, N, R, A = 64, 136, 16, 2
+    s = make(M, K, N, R, A, "fp16", bias=False)
+    s["w"].zero_()
+    s["x"] = (s["x"].float() * tsize ** 0.5).half()
+    s["a"] = (s["a"].float() * tsize ** 0.5).half()
+    s["b"] = (s["b"].float() * bsize / (0.5 * R ** -0.5)).half()
+    y = run(ug, s)
+    x, a, b = (s[k].double() for k in ("x", "a", "b"))
+    want, tol = torch.zeros(M, N, dtype=torch.float64, device="cuda"), torch.zeros(M, N, dtype=torch.float64, device="cuda")
+    for i in range(A):
+        m = (s["ids"] == i).nonzero().squeeze(1)
+        f = s["scales"][i].double()
+        t, mag = f * (x[m] @ a[i].T), f * (x[m].abs() @ a[i].abs().T)
+        want[m] = t @ b[i].T
+        tb = t.abs()[:, None] * b[i].abs()[None]               # [rows, N, R]
+        off = 2.0 ** -22 * tb + 2.0 ** -36 * b[i].abs() + torch.minimum(2.0 ** -26 * t.abs()[:, None], 2.0 ** -12 * tb)
+        tol[m] = off.sum(-1) + (2 * K + 2 * R) * 2.0 ** -23 * (mag @ b[i].abs().T)
+    check(y, want, tol + 2.0 ** -11 * want.abs() + 2.0 ** -25)
