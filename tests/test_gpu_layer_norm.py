@@ -295,6 +295,63 @@ def test_gradients_against_differences(ug):
         assert abs((got.double() * d).sum() - slope) <= (ref[1] * d.abs()).sum() + extra.sum() + 1e-7 * slope.abs()
 
 
+# Rows enough for a warp to a row (64 to each of 148 multiprocessors): row ends inside and at a lane's piece,
+# and one to sixteen pieces of it; samples that end between the two rows of a pair.
+MANY = [(3, 3333, 516), (1, 10000, 1024), (3, 3200, 1028), (2, 5000, 1536), (7, 1400, 2044), (1, 9999, 2048)]
+
+
+@pytest.mark.parametrize("weight", ["none", "shared", "sample"])
+@pytest.mark.parametrize("dtype,wdtype", [("bf16", "bf16"), ("bf16", "fp32"), ("fp16", "fp16"), ("fp16", "fp32")])
+@pytest.mark.parametrize("shape", MANY)
+def test_many_rows(ug, shape, dtype, wdtype, weight):
+    run(ug, *shape, dtype, weight, wdtype, plus=weight == "sample")
+
+
+@pytest.mark.parametrize("shape,dtype", [((3, 3333, 515), "bf16"), ((2, 5000, 1153), "fp32"), ((1, 400, 16384), "bf16"), ((2, 300, 8191), "fp16"),
+                                         ((1, 5000, 4096), "bf16"), ((2, 5000, 2052), "fp16"), ((1, 10000, 640), "fp32")])
+def test_many_rows_of_other_widths_and_types(ug, shape, dtype):
+    run(ug, *shape, dtype, "sample", plus=True)
+
+
+@pytest.mark.parametrize("C", [516, 1536, 2048])
+def test_many_rows_in_place_and_a_row_of_nan(ug, C):
+    """Rows apart and y over x; a row of NaN changes no other row's bits; what lies between the rows stays."""
+    import torch
+    B, R = 2, 5000
+    x, _, w, b = make(B, R, C, "bf16", "sample", "fp32")
+    x[1, 77, C // 3] = float("nan")
+    want, mean, rstd = torch.empty_like(x), torch.empty(B, R, device="cuda"), torch.empty(B, R, device="cuda")
+    ug.layer_norm(x, want, w, b, mean=mean, rstd=rstd)
+    rest = torch.ones(B, R, dtype=torch.bool, device="cuda")
+    rest[1, 77] = False
+    clean = x.clone()
+    clean[1, 77] = 0
+    ry, rm, rr = forward_reference(clean, w, b, 0.0, 1e-6, x.dtype)
+    assert torch.isnan(want[1, 77]).all() and torch.isnan(mean[1, 77])
+    for name, got, ref in (("y", want, ry), ("mean", mean, rm), ("rstd", rstd, rr)):
+        check(name, got[rest], [t.expand_as(got)[rest] for t in ref])
+    big = torch.full((R, B, C + 8), 7.0, dtype=x.dtype, device="cuda")
+    v = big[..., :C].transpose(0, 1)
+    v.copy_(x)
+    ug.layer_norm(v, v, w, b)
+    assert torch.equal(v[rest], want[rest]) and torch.isnan(v[1, 77]).all() and (big[..., C:] == 7).all()
+
+
+def test_one_row_for_all(ug):
+    """x and dy of stride zero."""
+    import torch
+    x, dy, w, b = make(3, 40, 200, "bf16", "shared")
+    for xx, dd in ((x[:1].expand_as(x), dy), (x[:, :1].expand_as(x), dy[:1, :1].expand_as(dy))):
+        y, mean, rstd = torch.empty_like(dy), torch.empty(3, 40, device="cuda"), torch.empty(3, 40, device="cuda")
+        ug.layer_norm(xx, y, w, b, mean=mean, rstd=rstd)
+        check("y", y, forward_reference(xx, w, b, 0.0, 1e-6, x.dtype)[0])
+        dx, dw = torch.empty_like(dy), torch.empty(200, device="cuda")
+        ug.layer_norm_backward(dd, xx, mean, rstd, dx, w, dweight=dw)
+        rx, rw, _ = backward_reference(dd, xx, mean, rstd, w, 0.0, x.dtype, torch.float32, False)
+        check("dx", dx, rx)
+        check("dw", dw, rw)
+
+
 def test_calls_of_several_threads_that_take_unequal_shared_memory(ug):
     """The same kernel for many rows and for few, from host threads at once (through the C call, which runs
     without Python's lock): each launch is accepted."""
