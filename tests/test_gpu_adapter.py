@@ -250,3 +250,57 @@ def test_fp16_products_of_unequal_sizes(ug, M, tsize, bsize):
         off = 2.0 ** -22 * tb + 2.0 ** -36 * b[i].abs() + torch.minimum(2.0 ** -26 * t.abs()[:, None], 2.0 ** -12 * tb)
         tol[m] = off.sum(-1) + (2 * K + 2 * R) * 2.0 ** -23 * (mag @ b[i].abs().T)
     check(y, want, tol + 2.0 ** -11 * want.abs() + 2.0 ** -25)
+
+
+# Tiles of 256 columns, several to a pair of blocks, as a layer's projections take them (74 pairs), and
+# several of 128; rows and columns that end inside a tile.
+LAYERS = [(9728, 136, 4608, 16, 5), (9700, 64, 4600, 32, 2), (4864, 1536, 1536, 16, 2), (20000, 72, 1001, 24, 3), (5000, 320, 2048, 64, 4)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("ids", ["mixed", "late", "runs"])
+@pytest.mark.parametrize("shape", LAYERS)
+def test_layers(ug, shape, ids, dtype):
+    s = make(*shape, dtype, ids=ids, bias=ids != "runs")
+    check(run(ug, s), *reference(s))
+
+
+@pytest.mark.parametrize("shape", LAYERS[:2])
+def test_infinities_and_nan_of_an_adapter_in_a_layer(ug, shape):
+    """As above with few tiles, here with the flags of tiles that follow one another in a block."""
+    import torch
+    M, _, N, R, A = shape
+    s = make(*shape, "bf16")
+    s["ids"][M // 3:M // 2] = 0                                # tiles without the sick adapter between tiles with it
+    ref, tol = reference(s)
+    s["b"][1, 5, 3] = float("inf")
+    s["b"][1, N // 2:N // 2 + 40] = float("nan")
+    s["b"][1, N - 1, R - 1] = float("-inf")
+    y = run(ug, s)
+    cols = torch.zeros(N, dtype=torch.bool, device="cuda")
+    cols[5] = cols[N - 1] = True
+    cols[N // 2:N // 2 + 40] = True
+    hit = (s["ids"] == 1)[:, None] & cols[None]
+    assert not torch.isfinite(y[hit]).any()
+    assert ((y.double() - ref).abs() <= tol)[~hit].all()
+
+
+def test_same_bits_in_a_layer(ug):
+    import torch
+    s = make(*LAYERS[0], "bf16")
+    first = run(ug, s)
+    side, noise = torch.cuda.Stream(), torch.randn(2048, 2048, device="cuda")
+    for i in range(10):
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            for _ in range(i):
+                noise = (noise @ noise).tanh()
+        assert torch.equal(first, run(ug, s))
+
+
+@pytest.mark.parametrize("M", [20, 400])
+def test_one_row_for_all(ug, M):
+    """x of stride zero: the same row for every adapter."""
+    s = make(M, 128, 136, 16, 3, "bf16")
+    s["x"] = s["x"][:1].expand(M, 128)
+    check(run(ug, s), *reference(s))
