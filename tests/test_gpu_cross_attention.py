@@ -378,3 +378,72 @@ def test_long_states_past_32_bit_offsets(ug):
     check("dq", dq, *ref["dq"])
     check("dk", dkf, *ref["dk"])
     check("dv", dv, *ref["dv"])
+
+
+# More work items than multiprocessors in every kernel, so that blocks go from item to item (accumulators,
+# barriers and constants handed over), as a layer's sizes have it.  At 148 multiprocessors: two query tiles
+# to an item, the last with one; heads that share keys (42 queries to a tile); all keys in one tile; two
+# samples' key tiles to a block; split keys (4 parts) and split queries (4 parts) with several items a block.
+LAYERS = [(4, 600, 300, 24, 24, 128), (4, 600, 300, 24, 24, 64), (4, 700, 260, 24, 8, 128), (3, 1100, 520, 16, 4, 64),
+          (4, 1300, 77, 24, 24, 128), (8, 130, 1000, 16, 16, 128), (10, 20, 4096, 15, 15, 64), (10, 20, 4096, 15, 15, 128),
+          (10, 4096, 100, 15, 15, 128), (10, 4096, 100, 15, 15, 64)]
+
+
+def prompts(B, S):
+    """Lengths of padded prompts, an empty one and one of a single state among them."""
+    return [(S, 0, 1, S // 2 + 1, S - 1)[i % 5] for i in range(B)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("hidden", ["nothing", "lengths", "scattered", "late and lengths"])
+@pytest.mark.parametrize("shape", LAYERS)
+def test_several_items_to_a_block(ug, shape, hidden, dtype):
+    lens = prompts(shape[0], shape[2]) if "lengths" in hidden else None
+    mask = {"scattered": _scatter, "late and lengths": _late}.get(hidden)
+    run(ug, *shape, dtype, lens=lens, mask=mask)
+
+
+@pytest.mark.parametrize("shape", LAYERS)
+def test_same_bits_with_several_items_to_a_block(ug, shape):
+    """Ten runs beside other work of unequal length, which shifts the blocks' timing."""
+    import torch
+    B, N, S, H, G, D = shape
+    q, k, v, do = inputs(*shape, torch.bfloat16)
+    lens = torch.tensor(prompts(B, S), dtype=torch.int32, device="cuda")
+    side, noise = torch.cuda.Stream(), torch.randn(2048, 2048, device="cuda")
+    first = None
+    for i in range(10):
+        o, lse = torch.full_like(q, float("nan")), torch.full((B, H, N), float("nan"), device="cuda")
+        dq, dk, dv = (torch.full_like(t, float("nan")) for t in (q, k, v))
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            for _ in range(i):
+                noise = (noise @ noise).tanh()
+        ug.cross_attention(q, k, v, o, kv_lens=lens, lse=lse)
+        ug.cross_attention_backward(do, q, k, v, o, lse, dq, dk, dv, kv_lens=lens)
+        torch.cuda.synchronize()
+        assert ug.operator_status() == 0
+        got = (o, lse, dq, dk, dv)
+        first = first or got
+        assert [int((a != b).sum()) for a, b in zip(first, got)] == [0] * 5
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_broadcast_inputs(ug, D):
+    """Strides of zero: one prompt for all samples, one key/value head for all, one do for all queries; the
+    gradients come for each of them."""
+    import torch
+    B, N, S, H, dt = 3, 150, 140, 4, torch.bfloat16
+    q, k, v, do = inputs(B, N, S, H, H, D, dt)
+    for kk, vv, dd in ((k[:1].expand_as(k), v[:1].expand_as(v), do), (k[:, :, :1].expand_as(k), v, do[:, :1].expand_as(do)),
+                       (k, v[:1, :, :1].expand_as(v), do[:1, :1, :1].expand_as(do))):
+        ref = reference(q, kk, vv, dd, None, None, D ** -0.5)
+        o, lse = torch.full_like(q, float("nan")), torch.full((B, H, N), float("nan"), device="cuda")
+        ug.cross_attention(q, kk, vv, o, lse=lse)
+        check("o", o, *ref["o"])
+        check("lse", lse, *ref["lse"])
+        dq, dk, dv = (torch.full_like(t, float("nan")) for t in (q, k, v))
+        ug.cross_attention_backward(dd, q, kk, vv, o, lse, dq, dk, dv)
+        check("dv", dv, *ref["dv"])
+        check("dk", dk, *ref["dk"])
+        check("dq", dq, *ref["dq"])
