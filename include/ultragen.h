@@ -515,7 +515,9 @@ int ultragen_adapter_project(const ultragen_adapter_t* c, const void* x, const v
  *   the forward pass wrote them.  Hidden keys and values get zeros; a query without a visible
  *   key gets dq = 0.  dk and dv of a shared head are summed over its query heads.  Results do
  *   not depend on timing (no atomics on the outputs).
- * Products run on 16-bit tensor cores with fp32 sums; softmax statistics are fp32.  batch, nq or
+ * Products run on 16-bit tensor cores with fp32 sums; softmax statistics are fp32.  p, and backward
+ * p (do . v - do . o), are rounded to the 16-bit type for them: in fp16 the latter must stay below 65,504
+ * (a scaled loss), and is off by 2^-25 at least.  batch, nq or
  * ns = 0 is allowed (outputs that exist are written).  workspace: `backward` selects the call.
  *   INVALID_ARG: null pointers, negative sizes, heads not a multiple of kv_heads, misaligned
  *   strides, too little workspace.  UNSUPPORTED: another dtype or head_dim (64, 128), more than

@@ -447,3 +447,50 @@ def test_broadcast_inputs(ug, D):
         check("dv", dv, *ref["dv"])
         check("dk", dk, *ref["dk"])
         check("dq", dq, *ref["dq"])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("size", [512.0, 2.0 ** -10])
+def test_scaled_losses(ug, size, dtype):
+    """do of another size, as a scaled loss or a mean over many tokens gives it."""
+    import torch
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float16
+    B, N, S, H, G, D = 2, 300, 260, 4, 2, 128
+    q, k, v, do = inputs(B, N, S, H, G, D, dt)
+    do = (do.float() * size).to(dt)
+    ref = reference(q, k, v, do, None, None, D ** -0.5)
+    o, lse = torch.empty_like(q), torch.empty(B, H, N, device="cuda")
+    ug.cross_attention(q, k, v, o, lse=lse)
+    dq, dk, dv = (torch.full_like(t, float("nan")) for t in (q, k, v))
+    ug.cross_attention_backward(do, q, k, v, o, lse, dq, dk, dv)
+    check("dv", dv, *ref["dv"])
+    check("dk", dk, *ref["dk"])
+    check("dq", dq, *ref["dq"])
+
+
+def test_both_passes_on_two_streams_at_once(ug):
+    import torch
+    sets = []
+    for seed in range(2):
+        q, k, v, do = inputs(3, 500, 400, 8, 4, 128, torch.bfloat16, seed)
+        lens, mask = torch.tensor([400, 77, 0], dtype=torch.int32, device="cuda"), _scatter(3, 400).cuda()
+
+        def once(out, a=(q, k, v, do, lens, mask), stream=None):
+            q, k, v, do, lens, mask = a
+            ug.cross_attention(q, k, v, out[0], kv_lens=lens, key_mask=mask, lse=out[1], stream=stream)
+            ug.cross_attention_backward(do, q, k, v, out[0], out[1], *out[2:], kv_lens=lens, key_mask=mask, stream=stream)
+        outs = [(torch.empty_like(q), torch.empty(3, 8, 500, device="cuda"), torch.empty_like(q), torch.empty_like(k), torch.empty_like(v))
+                for _ in range(9)]
+        once(outs[0])
+        sets.append((once, outs, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for i in range(1, 9):
+        for once, outs, stream in sets:
+            once(outs[i], stream=stream)
+    torch.cuda.synchronize()
+    assert ug.operator_status() == 0
+    assert all(torch.equal(a, b) for _, outs, _ in sets for out in outs[1:] for a, b in zip(outs[0], out))
+
+
+def test_more_samples_than_a_grid_dimension_holds(ug):
+    run(ug, 70000, 2, 130, 1, 1, 64, "bf16", poison=False)
