@@ -304,3 +304,16 @@ def test_one_row_for_all(ug, M):
     s = make(M, 128, 136, 16, 3, "bf16")
     s["x"] = s["x"][:1].expand(M, 128)
     check(run(ug, s), *reference(s))
+
+
+@pytest.mark.parametrize("M", [7, 8, 9, 16, 17, 32, 33, 64, 65, 255, 256, 513])
+def test_row_counts_at_the_kernels_borders(ug, M):
+    s = make(M, 520, 300, 16, 8, "bf16")
+    check(run(ug, s), *reference(s))
+
+
+@pytest.mark.parametrize("M", [577, 1000, 2000])
+@pytest.mark.parametrize("R", [16, 64])
+def test_several_adapters_in_some_hundreds_of_rows(ug, M, R):
+    s = make(M, 512, 520, R, 8, "fp16")
+    check(run(ug, s), *reference(s))

@@ -352,6 +352,34 @@ def test_one_row_for_all(ug):
         check("dw", dw, rw)
 
 
+@pytest.mark.parametrize("shape", [(1, 9471, 1024), (1, 9472, 1024), (65535, 1, 64), (4001, 3, 520)])
+def test_row_and_sample_counts_at_the_kernels_borders(ug, shape):
+    run(ug, *shape, "bf16", "sample", "fp32", plus=True)
+
+
+def test_two_streams_at_once(ug):
+    import torch
+    sets = []
+    for seed in range(2):
+        x, dy, w, b = make(2, 4000, 1536, "bf16", "shared", "fp32", seed=seed)
+
+        def once(o, a=(x, dy, w, b), stream=None):
+            x, dy, w, b = a
+            ug.layer_norm(x, o[0], w, b, mean=o[1], rstd=o[2], stream=stream)
+            ug.layer_norm_backward(dy, x, o[1], o[2], o[3], w, dweight=o[4], dbias=o[5], stream=stream)
+        outs = [[torch.empty_like(x), torch.empty(2, 4000, device="cuda"), torch.empty(2, 4000, device="cuda"), torch.empty_like(x),
+                 torch.empty(1536, device="cuda"), torch.empty(1536, device="cuda")] for _ in range(9)]
+        once(outs[0])
+        sets.append((once, outs, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for i in range(1, 9):
+        for once, outs, stream in sets:
+            once(outs[i], stream=stream)
+    torch.cuda.synchronize()
+    assert ug.operator_status() == 0
+    assert all(torch.equal(a, c) for _, outs, _ in sets for o in outs[1:] for a, c in zip(outs[0], o))
+
+
 def test_calls_of_several_threads_that_take_unequal_shared_memory(ug):
     """The same kernel for many rows and for few, from host threads at once (through the C call, which runs
     without Python's lock): each launch is accepted."""
