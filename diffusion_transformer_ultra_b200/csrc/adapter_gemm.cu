@@ -12,8 +12,10 @@
 // Roles per CTA (10 warps): 0-3 epilogue (TMEM -> 16 bits -> shared memory -> rows of y), 4 TMA
 // producer, 5 MMA issuer (first CTA of the pair), 6-9 extension: writes the granules.
 // TMEM: two accumulators of BN columns, so that a tile's epilogue runs beside the next products.
-// 9,728 x 1,536 -> 4,608: 100 us, 1.38 PF/s; 70,144 x 2,048 -> 2,048 with rank 32: 407 us, 1.49 PF/s
-// (a library product reaches 1.63 in a burst, 1.39 over seconds): bound by the tensor pipe.
+// With the kernel that makes t, of which the second case hides little: 9,728 x 1,536 -> 4,608, 105 us,
+// 1.31 PF/s, in a burst of calls; 70,144 x 2,048 -> 2,048 with rank 32, 529 us, of which t takes 103 to 126.
+// In a loop of seconds 124 and 606 us: the power limit holds the clock at 1,552 and 1,395 of 1,965 MHz.  (A
+// library product reaches 1.63 PF/s in a burst, 1.39 over seconds.)
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

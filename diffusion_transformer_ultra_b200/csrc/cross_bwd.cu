@@ -74,8 +74,8 @@ __device__ __forceinline__ float neg_lse2(float lse) { return lse == neg_inf() ?
 // 512 threads: warps 10 (scrubber: zeroes hidden K rows, which may hold NaN: 0 * NaN), 12-15 (the
 // accumulators' way to dq: the elementwise warps are what a step waits for).  delta = do . o comes from
 // a kernel before: made by warps 12-15 in here, its code and the other roles' did not fit the
-// instruction cache together (156 misses a step), and the pass took 218 us.  Now it takes 122, 808 TF/s,
-// and delta 27, 5.6 TB/s, for 4 x 4,096 queries, 512 keys (436, 359 and none in three samples), 24 heads
+// instruction cache together (156 misses a step), and the pass took 218 us.  Now it takes 119, 826 TF/s,
+// and delta 27, 5.7 TB/s, for 4 x 4,096 queries, 512 keys (436, 359 and none in three samples), 24 heads
 // of 128; bound by the elementwise warps' chain of loads, exponentials and stores.
 // TMEM: S [0,128), dP / dS in two buffers [128,384), dQ [384,384+D).
 template <int D>
@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(256) cross_delta_kernel(const CrossParams p) {
 // in registers writes P^T and dS^T (16 bits, 32 columns each) over it, so that S^T is free as soon
 // as it is read and the next S^T is made beside this step's exponentials; with P^T over S^T a step waits
 // for its own dV product and the next S^T.  4 x 4,096 queries, 512 keys (436, 359 and none in three
-// samples), 24 heads of 128: 147 us, 895 TF/s; tensor pipe about 55% busy, bound by a step's chain
+// samples), 24 heads of 128: 132 us, 995 TF/s; tensor pipe about half busy, bound by a step's chain
 // of product, exponentials, product.
 template <int D>
 struct CfgK {

@@ -9,9 +9,11 @@
 //   warps 12-15     output: O from TMEM to memory, beside the next item's first softmax.  An encoder's
 //                   states are a few key tiles (4 for 512), so items are short: with this in the
 //                   softmax warps it took 5,000 of an item's 19,000 cycles.
-// 65,536 queries x 512 keys x 24 heads of 128: 400 us, 1,030 TF/s.  A tile's chain of product,
-// exponentials and product bounds it, two tiles to a CTA against each other: TMEM has no room for a
-// third S at this head size.
+// 65,536 queries x 512 keys x 24 heads of 128: 415 us, 993 TF/s, in a burst of calls; in a loop of seconds
+// 484 us, 852 TF/s, where the power limit holds the clock at 1,612 of 1,965 MHz.  A tile's chain of product,
+// exponentials and product bounds it, two tiles to a CTA against each other (TMEM has no room for a third S
+// at this head size), and items are short: one key tile in four is an item's first, whose S is read twice
+// (maximum, exponentials), and Q has one buffer.
 // TMEM (512 columns): S0 [0,128), S1 [128,256), O0 [256,256+D), O1 [256+D, 256+2D); P (16 bits,
 // packed in pairs, 64 columns in 32) overwrites the first and third quarter of its S block.
 #include <cstdint>

@@ -847,8 +847,10 @@ int ultragen_layer_norm(const ultragen_norm_t* n, const void* x, const void* wei
   a.rstd = rstd;
   const bool contig = contiguous_pieces(n, x, nullptr, y, weight, bias);
   Spread sp = spread(n->cols);
-  // A warp to a row where every warp has several; with fewer, warps that share a row are sooner done
-  // (rows of 2,048: 4,736 take 21.8 us by one warp each, 17.7 by four; 70,144 take 122 and 150).
+  // A warp to a row where every warp has several; with fewer, warps that share a row are sooner done.  In us,
+  // by a warp to a row and by warps that share one: rows of 2,048, 4,736 of them 15.1 and 13.7, 9,472 (the
+  // border) 25.3 and 23.5, 20,000 43.7 and 45.7, 70,144 113 and 150; rows of 516, 8.9 and 7.1, 12.2 and 11.4,
+  // 18.9 and 20.2, 55 and 62.  768, 1,024 and 1,536 columns lie between, with 4 to 11% lost at the border.
   a.wide = contig && n->dtype != ULTRAGEN_F32 && n->cols > 512 && n->cols <= 2048 && a.total >= 64 * (int64_t)sm_count();
   if (a.wide) sp.warps = 1;
   a.warps = sp.warps;
