@@ -118,6 +118,7 @@ __device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, u
       "setp.gt.s32 q, t, %5;\n\t"
       "add.u32 n, n, 1;\n\t"
       "setp.gt.and.u32 q, n, 2048, q;\n\t"
+      "setp.gt.or.u32 q, n, 67108864, q;\n\t"
       "@q st.volatile.shared.u32 [%3], %4;\n\t"
       "setp.ne.or.u32 q, f, 0, q;\n\t"
       "@!q bra LOOP_%=;\n\t"

@@ -33,3 +33,9 @@ def test_time_and_looks(over, t0):
         assert not over(at(-back), t0, 10 ** 6)
     for ahead in (LIMIT + 1, 3600 * SECOND):                   # stepped forward: the first looks do not end it
         assert not over(at(ahead), t0, 1) and not over(at(ahead), t0, 2047)
+
+
+def test_a_timer_stepped_far_back_does_not_hold_a_wait(over):
+    t0 = 1_700_000_000 * SECOND
+    back = t0 - 24 * 3600 * SECOND
+    assert not over(back, t0, 2 ** 26 - 1) and over(back, t0, 2 ** 26) and over(t0, t0, 2 ** 26)
